@@ -664,6 +664,162 @@ int fdl_full_attention(fdl_ctx* ctx, const fdl_attn_desc* desc, const void* q,
 
 }  // extern "C"
 
+// ---- 4-bit K/V cache ---------------------------------------------------------------
+namespace {
+
+int check_kv4_cache(const char* who, const fdl_kv4_cache* c) {
+    if (!c || !c->k || !c->k_scale || !c->v || !c->v_scale)
+        return fail(FDL_EINVAL, "%s: cache or one of its buffers is NULL", who);
+    if (!aligned16(c->k) || !aligned16(c->k_scale) || !aligned16(c->v) || !aligned16(c->v_scale))
+        return fail(FDL_EINVAL, "%s: the cache's buffers must be 16-byte aligned", who);
+    return FDL_OK;
+}
+
+fdl::Kv4Ptrs kv4_ptrs(const fdl_kv4_cache* c) {
+    return fdl::Kv4Ptrs{(uint8_t*)c->k, (uint8_t*)c->k_scale, (uint8_t*)c->v,
+                        (uint8_t*)c->v_scale};
+}
+
+// Checks the rows [start, start + n) of a store or load and resolves their strides.
+int kv4_rows(const char* who, const fdl_ctx* ctx, const fdl_kv4_rows_desc* d, int start, int n,
+             bool written, fdl::Kv4Rows* out) {
+    if (!ctx) return fail(FDL_EINVAL, "%s: ctx is NULL", who);
+    if (!d) return fail(FDL_EINVAL, "%s: desc is NULL", who);
+    if (d->batch < 1 || d->batch > 65535 || d->n_kv_heads < 1 || d->seq_len < 1)
+        return fail(FDL_EINVAL, "%s: batch must be in [1, 65535], n_kv_heads and seq_len >= 1",
+                    who);
+    if (d->head_dim != 64 && d->head_dim != 128)
+        return fail(FDL_EUNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", who,
+                    d->head_dim);
+    if (d->dtype != FDL_F32 && d->dtype != FDL_BF16)
+        return fail(FDL_EINVAL, "%s: unknown dtype %d", who, d->dtype);
+    if (n < 1 || start < 0 || (int64_t)start + n > d->seq_len)
+        return fail(FDL_EINVAL, "%s: rows [%d, %lld) outside [0, %d)", who, start,
+                    (long long)start + n, d->seq_len);
+    // the kernels count the 16-byte pieces of a sequence's rows in 31 bits
+    if ((int64_t)d->n_kv_heads * n * d->head_dim >= ((int64_t)1 << 33))
+        return fail(FDL_EUNSUPPORTED, "%s: %d heads x %d rows are too many for one call", who,
+                    d->n_kv_heads, n);
+    fdl::Kv4Rows r{d->batch, d->n_kv_heads, d->head_dim, d->seq_len, start, n,
+                   d->dtype == FDL_BF16 ? 1 : 0, d->seq_stride, d->row_stride, d->head_stride};
+    if (!r.seq_stride && !r.row_stride && !r.head_stride) {
+        r.head_stride = d->head_dim;
+        r.row_stride = (long long)d->n_kv_heads * d->head_dim;
+        r.seq_stride = r.row_stride * n;
+    }
+    const int per16 = r.bf16 ? 8 : 4;
+    if (r.seq_stride < 0 || r.row_stride < 0 || r.head_stride < 0 || r.seq_stride % per16 ||
+        r.row_stride % per16 || r.head_stride % per16)
+        return fail(FDL_EINVAL, "%s: strides must be >= 0 and multiples of 16 bytes", who);
+    if (written && ((r.batch > 1 && !r.seq_stride) || (n > 1 && r.row_stride < r.head_dim) ||
+                    (r.heads > 1 && r.head_stride < r.head_dim)))
+        return fail(FDL_EINVAL, "%s: the rows written must not overlap", who);
+    *out = r;
+    return FDL_OK;
+}
+
+int check_kv4_attn(const fdl_kv4_attn_desc* d, fdl::Kv4Attn* out) {
+    if (!d) return fail(FDL_EINVAL, "kv4_attention: desc is NULL");
+    if (d->block_start < 0 || (int64_t)d->block_start + d->block_len > d->seq_len)
+        return fail(FDL_EINVAL, "kv4_attention: block [%d, %lld) outside [0, %d)", d->block_start,
+                    (long long)d->block_start + d->block_len, d->seq_len);
+    const fdl_attn_desc ad{d->batch, d->n_q_heads, d->n_kv_heads, d->head_dim, d->seq_len,
+                           d->block_start, d->block_len, d->dtype, d->scale};
+    const int rc = check_attn(&ad);
+    if (rc) return rc;
+    if (d->dtype != FDL_BF16)
+        return fail(FDL_EUNSUPPORTED, "kv4_attention: q and out must be bf16");
+    if (d->sinks < 0) return fail(FDL_EINVAL, "kv4_attention: sinks must be >= 0");
+    if ((int64_t)d->batch * d->n_q_heads * d->block_len >= ((int64_t)1 << 28))
+        return fail(FDL_EUNSUPPORTED, "kv4_attention: too many query rows for one call");
+    const int64_t lo = d->window_left < 0 ? 0 : (int64_t)d->block_start - d->window_left;
+    const int64_t hi = d->window_right < 0 ? d->seq_len
+        : (int64_t)d->block_start + d->block_len + d->window_right;
+    fdl::Kv4Attn s{};
+    s.batch = d->batch;
+    s.n_q_heads = d->n_q_heads;
+    s.n_kv_heads = d->n_kv_heads;
+    s.head_dim = d->head_dim;
+    s.seq_len = d->seq_len;
+    s.block_len = d->block_len;
+    s.sinks = d->sinks < d->seq_len ? d->sinks : d->seq_len;
+    s.win_lo = lo > 0 ? (int)lo : 0;
+    s.win_hi = hi < d->seq_len ? (int)hi : d->seq_len;
+    s.scale = d->scale == 0.f ? 1.0f / sqrtf((float)d->head_dim) : d->scale;
+    *out = s;
+    return FDL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fdl_kv4_store(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const void* k_new,
+                  const void* v_new, int start, int n, const fdl_kv4_cache* cache, void* stream) {
+    fdl::Kv4Rows r;
+    int rc = kv4_rows("kv4_store", ctx, desc, start, n, false, &r);
+    if (!rc) rc = check_kv4_cache("kv4_store", cache);
+    if (rc) return rc;
+    if (!k_new || !v_new) return fail(FDL_EINVAL, "kv4_store: NULL buffer");
+    if (!aligned16(k_new) || !aligned16(v_new))
+        return fail(FDL_EINVAL, "kv4_store: k_new and v_new must be 16-byte aligned");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(FDL_ECUDA, "kv4_store: cannot select device");
+    const cudaError_t e = fdl::launch_kv4_store(r, k_new, v_new, kv4_ptrs(cache),
+                                                (cudaStream_t)stream);
+    return e == cudaSuccess ? FDL_OK : cuda_fail(e, "kv4_store launch");
+}
+
+int fdl_kv4_load(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const fdl_kv4_cache* cache,
+                 int start, int n, void* k_out, void* v_out, void* stream) {
+    fdl::Kv4Rows r;
+    int rc = kv4_rows("kv4_load", ctx, desc, start, n, true, &r);
+    if (!rc) rc = check_kv4_cache("kv4_load", cache);
+    if (rc) return rc;
+    if (!k_out && !v_out) return fail(FDL_EINVAL, "kv4_load: k_out and v_out are both NULL");
+    if (!aligned16(k_out) || !aligned16(v_out))
+        return fail(FDL_EINVAL, "kv4_load: k_out and v_out must be 16-byte aligned");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(FDL_ECUDA, "kv4_load: cannot select device");
+    const cudaError_t e = fdl::launch_kv4_load(r, kv4_ptrs(cache), k_out, v_out,
+                                               (cudaStream_t)stream);
+    return e == cudaSuccess ? FDL_OK : cuda_fail(e, "kv4_load launch");
+}
+
+size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx, const fdl_kv4_attn_desc* desc) {
+    if (!ctx) { fail(FDL_EINVAL, "kv4_attention workspace: ctx is NULL"); return 0; }
+    fdl::Kv4Attn s;
+    if (check_kv4_attn(desc, &s) != FDL_OK) return 0;
+    return fdl::kv4_attention_workspace_bytes(s, ctx->sm_count);
+}
+
+int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q,
+                      const fdl_kv4_cache* cache, const int32_t* kv_len, void* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream) {
+    if (!ctx) return fail(FDL_EINVAL, "kv4_attention: ctx is NULL");
+    fdl::Kv4Attn s;
+    int rc = check_kv4_attn(desc, &s);
+    if (!rc) rc = check_kv4_cache("kv4_attention", cache);
+    if (rc) return rc;
+    if (!q || !out) return fail(FDL_EINVAL, "kv4_attention: q and out must be non-NULL");
+    if (q == out) return fail(FDL_EINVAL, "kv4_attention: out must not be q");
+    if (!aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3u) || ((uintptr_t)kv_len & 3u))
+        return fail(FDL_EINVAL, "kv4_attention: q and out must be 16-byte aligned, lse and "
+                    "kv_len 4-byte aligned");
+    const size_t need = fdl::kv4_attention_workspace_bytes(s, ctx->sm_count);
+    if (!ws || ws_bytes < need || !aligned16(ws))
+        return fail(FDL_EWORKSPACE, "kv4_attention: workspace needs %zu bytes (16-byte aligned), "
+                    "got %zu", need, ws ? ws_bytes : (size_t)0);
+    s.kv_len = kv_len;
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(FDL_ECUDA, "kv4_attention: cannot select device");
+    const cudaError_t e = fdl::launch_kv4_attention(s, q, kv4_ptrs(cache), out, lse, ws,
+                                                    ctx->sm_count, (cudaStream_t)stream);
+    return e == cudaSuccess ? FDL_OK : cuda_fail(e, "kv4_attention launch");
+}
+
+}  // extern "C"
+
 // ---- the whole decode ------------------------------------------------------------
 struct fdl_model {
     uint64_t id;              // unique per fdl_model_create (keys the cached decode graph)

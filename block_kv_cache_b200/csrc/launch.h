@@ -66,6 +66,34 @@ cudaError_t launch_kv_store(int batch, int n_kv_heads, int head_dim, int seq_len
                             int start, int n, void* k_cache, void* v_cache,
                             cudaStream_t st);
 
+// ---- the 4-bit K/V cache -------------------------------------------------------
+// Codes [b, Hkv, L, d/2] and scales [b, Hkv, L, d/16] (kv4.cuh).
+struct Kv4Ptrs { uint8_t *k, *k_scale, *v, *v_scale; };
+
+// Rows [start, start + n) of every sequence and head; the unquantised rows lie
+// at seq * seq_stride + position * row_stride + head * head_stride elements.
+struct Kv4Rows {
+    int batch, heads, head_dim, seq_len, start, n, bf16;
+    long long seq_stride, row_stride, head_stride;
+};
+cudaError_t launch_kv4_store(const Kv4Rows& s, const void* k_new, const void* v_new,
+                             const Kv4Ptrs& c, cudaStream_t st);
+cudaError_t launch_kv4_load(const Kv4Rows& s, const Kv4Ptrs& c, void* k_out, void* v_out,
+                            cudaStream_t st);
+
+// Attention of the block [block_start, block_start + block_len) over the
+// positions j < kv_len[sequence] (all L without kv_len) with j < sinks or
+// win_lo <= j < win_hi.
+struct Kv4Attn {
+    int batch, n_q_heads, n_kv_heads, head_dim, seq_len, block_len;
+    int sinks, win_lo, win_hi;   // 0 <= win_lo <= win_hi <= L, 0 <= sinks <= L
+    float scale;                 // resolved (never 0)
+    const int32_t* kv_len;
+};
+size_t kv4_attention_workspace_bytes(const Kv4Attn& s, int sm_count);
+cudaError_t launch_kv4_attention(const Kv4Attn& s, const void* q, const Kv4Ptrs& c, void* out,
+                                 float* lse, void* ws, int sm_count, cudaStream_t st);
+
 struct LMShape { int rows, hidden, vocab; };
 size_t lmhead_workspace_bytes(const LMShape& s);
 cudaError_t launch_lmhead_f32(const LMShape& s, const float* h, const float* w,

@@ -12,6 +12,7 @@ Layouts follow include/fdllm.h:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -33,7 +34,9 @@ EXPORTS = ("fdl_abi_version", "fdl_create", "fdl_destroy", "fdl_last_error",
            "fdl_lmhead_confidence_noalloc", "fdl_rope_table", "fdl_rmsnorm", "fdl_embed",
            "fdl_qkv_rope_store", "fdl_linear_residual", "fdl_linear_swiglu",
            "fdl_full_attention", "fdl_ffn", "fdl_qkv_attention", "fdl_model_create",
-           "fdl_model_destroy", "fdl_generate_workspace_bytes", "fdl_generate")
+           "fdl_model_destroy", "fdl_generate_workspace_bytes", "fdl_generate",
+           "fdl_kv4_store", "fdl_kv4_load", "fdl_kv4_attention_workspace_bytes",
+           "fdl_kv4_attention")
 
 
 class AttnDesc(ctypes.Structure):
@@ -44,7 +47,29 @@ class AttnDesc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
-ABI_VERSION = 6
+ABI_VERSION = 7
+
+
+class Kv4Buffers(ctypes.Structure):
+    """fdl_kv4_cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class Kv4RowsDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("seq_len", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("seq_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Kv4AttnDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("seq_len", ctypes.c_int), ("block_start", ctypes.c_int),
+                ("block_len", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_float), ("window_left", ctypes.c_int),
+                ("window_right", ctypes.c_int), ("sinks", ctypes.c_int)]
 
 
 class LMHeadDesc(ctypes.Structure):
@@ -156,6 +181,14 @@ def load() -> ctypes.CDLL:
     L.fdl_generate_workspace_bytes.restype = sz
     L.fdl_generate.argtypes = [vp, vp, vp, i, i, i, i, fl, ctypes.POINTER(GenerateOpts), vp,
                                ctypes.POINTER(i), vp, sz, vp]
+    L.fdl_kv4_store.argtypes = [vp, ctypes.POINTER(Kv4RowsDesc), vp, vp, i, i,
+                                ctypes.POINTER(Kv4Buffers), vp]
+    L.fdl_kv4_load.argtypes = [vp, ctypes.POINTER(Kv4RowsDesc), ctypes.POINTER(Kv4Buffers), i, i,
+                               vp, vp, vp]
+    L.fdl_kv4_attention_workspace_bytes.argtypes = [vp, ctypes.POINTER(Kv4AttnDesc)]
+    L.fdl_kv4_attention_workspace_bytes.restype = sz
+    L.fdl_kv4_attention.argtypes = [vp, ctypes.POINTER(Kv4AttnDesc), vp,
+                                    ctypes.POINTER(Kv4Buffers), vp, vp, vp, vp, sz, vp]
     for name in EXPORTS:
         getattr(L, name).restype = getattr(L, name).restype or i
     _lib = L
@@ -203,6 +236,38 @@ def rope_table(theta: float, max_pos: int, head_dim: int):
     _check(load().fdl_rope_table(float(theta), int(max_pos), int(head_dim),
                                  ctypes.c_void_p(out.ctypes.data)))
     return out
+
+
+class Kv4Cache:
+    """One layer's K/V cache in microscaled 4-bit floating point (fdl_kv4_cache): codes k, v
+    [b, Hkv, L, d/2] and scales k_scale, v_scale [b, Hkv, L, d/16], uint8 CUDA tensors that the
+    caller may own (Kv4Cache(k, k_scale, v, v_scale)) or have allocated here (Kv4Cache.empty,
+    zeroed: every position reads as 0 until it is stored)."""
+
+    def __init__(self, k, k_scale, v, v_scale):
+        for t, n in ((k, "k"), (k_scale, "k_scale"), (v, "v"), (v_scale, "v_scale")):
+            _need(t, n, torch.uint8, 4)
+            if t.device != k.device:
+                raise ValueError(f"{n} is on {t.device}, k on {k.device}")
+        b, h, L, half = k.shape
+        if half not in (32, 64):
+            raise ValueError(f"Kv4Cache: k has {half} code bytes per row, not 32 or 64 "
+                             "(head_dim 64 or 128)")
+        if v.shape != k.shape or k_scale.shape != (b, h, L, half // 8) \
+                or v_scale.shape != k_scale.shape:
+            raise ValueError(f"Kv4Cache: shapes {tuple(k.shape)}, {tuple(k_scale.shape)}, "
+                             f"{tuple(v.shape)}, {tuple(v_scale.shape)} do not belong together")
+        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        self.batch, self.n_kv_heads, self.seq_len, self.head_dim = b, h, L, 2 * half
+        self.buffers = Kv4Buffers(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
+                                  v_scale.data_ptr())
+
+    @classmethod
+    def empty(cls, batch, n_kv_heads, seq_len, head_dim=128, device="cuda"):
+        codes = (batch, n_kv_heads, seq_len, head_dim // 2)
+        scales = (batch, n_kv_heads, seq_len, head_dim // 16)
+        return cls(*(torch.zeros(s, dtype=torch.uint8, device=device)
+                     for s in (codes, scales, codes, scales)))
 
 
 class Model:
@@ -318,6 +383,140 @@ class Context:
         _check(load().fdl_kv_store(self._h, ctypes.byref(desc), _ptr(k_new), _ptr(v_new),
                                    int(start), int(n), _ptr(k_cache), _ptr(v_cache),
                                    _stream(stream)))
+
+    # -- 4-bit K/V cache ----------------------------------------------------
+    def _on(self, t, name, dtype=None, ndim=None):
+        """A CUDA tensor on this context's device (strides are looked at elsewhere)."""
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.device.index != self.device:
+            raise ValueError(f"{name} is on {t.device}, the context on cuda:{self.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if ndim is not None and t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+
+    def _at(self, stream):
+        """The stream of a call: `stream`, or the current one of this context's device."""
+        return stream if stream is not None else torch.cuda.current_stream(self.device)
+
+    @staticmethod
+    def _memory_of(stream):
+        """Tensors allocated inside belong to the stream of the call that writes them."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    def _kv4_rows(self, cache, k, v, n):
+        """Descriptor of unquantised rows k, v (either may be None) [b, n, Hkv, d]."""
+        one = k if k is not None else v
+        want = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
+        strides = None
+        for t, name in ((k, "k"), (v, "v")):
+            if t is None:
+                continue
+            self._on(t, name, one.dtype, 4)
+            if tuple(t.shape) != want:
+                raise ValueError(f"{name} rows have shape {tuple(t.shape)}, not {want}")
+            if t.stride(3) != 1:
+                raise ValueError(f"{name} rows must be contiguous along head_dim")
+            # a dimension of one position has no stride of its own
+            full = (n * want[2] * want[3], want[2] * want[3], want[3])
+            st = tuple(s if size > 1 else f for s, size, f in zip(t.stride(), want, full))
+            if strides is not None and st != strides:
+                raise ValueError("k and v rows must have the same strides")
+            strides = st
+        if not any(strides):
+            raise ValueError("rows without any stride are not supported")
+        return Kv4RowsDesc(cache.batch, cache.n_kv_heads, cache.head_dim, cache.seq_len,
+                           _dtype_code(one), *strides)
+
+    def kv4_store(self, k_new, v_new, cache: Kv4Cache, start, stream=None):
+        """Quantise rows k_new, v_new [b, n, Hkv, d] (bf16 or f32; any strides with head_dim
+        contiguous, the same for both) into positions [start, start + n) of the cache."""
+        self._on(cache.k, "cache")
+        self._on(k_new, "k_new", None, 4)
+        self._on(v_new, "v_new", None, 4)
+        n = k_new.shape[1]
+        d = self._kv4_rows(cache, k_new, v_new, n)
+        _check(load().fdl_kv4_store(self._h, ctypes.byref(d), _ptr(k_new), _ptr(v_new),
+                                    int(start), int(n), ctypes.byref(cache.buffers),
+                                    _stream(self._at(stream))))
+
+    def kv4_load(self, cache: Kv4Cache, start=0, n=None, *, dtype=torch.bfloat16, k_out=None,
+                 v_out=None, stream=None):
+        """The values positions [start, start + n) of the cache stand for (n: to the end):
+        (k, v) [b, n, Hkv, d], new tensors of `dtype` (bf16 or f32) or the given k_out and
+        v_out (of one of them alone, only that one is read)."""
+        self._on(cache.k, "cache")
+        n = cache.seq_len - int(start) if n is None else int(n)
+        s = self._at(stream)
+        if k_out is None and v_out is None:
+            if n < 1:
+                raise ValueError(f"kv4_load: {n} rows")
+            shape = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
+            with self._memory_of(stream):
+                k_out, v_out = (torch.empty(shape, dtype=dtype, device=cache.k.device)
+                                for _ in range(2))
+        d = self._kv4_rows(cache, k_out, v_out, n)
+        _check(load().fdl_kv4_load(self._h, ctypes.byref(d), ctypes.byref(cache.buffers),
+                                   int(start), n, _ptr(k_out), _ptr(v_out), _stream(s)))
+        return k_out, v_out
+
+    def kv4_attn_desc(self, q, cache: Kv4Cache, block_start, window=(-1, -1), sinks=0,
+                      scale=0.0) -> Kv4AttnDesc:
+        b, B, Hq, d = q.shape
+        if (b, d) != (cache.batch, cache.head_dim):
+            raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.batch} sequences "
+                             f"and head_dim {cache.head_dim}")
+        return Kv4AttnDesc(b, Hq, cache.n_kv_heads, d, cache.seq_len, int(block_start), B,
+                           _dtype_code(q), float(scale), int(window[0]), int(window[1]),
+                           int(sinks))
+
+    def kv4_attention_workspace_bytes(self, desc: Kv4AttnDesc) -> int:
+        return int(load().fdl_kv4_attention_workspace_bytes(self._h, ctypes.byref(desc)))
+
+    def kv4_attention(self, q, cache: Kv4Cache, block_start, *, kv_len=None, window=(-1, -1),
+                      sinks=0, out=None, lse=None, want_lse=False, scale=0.0, ws=None,
+                      stream=None):
+        """Block attention over a 4-bit cache (fdl_kv4_attention). q [b, B, Hq, d] bf16, the
+        block's rows being in the cache already (kv4_store). kv_len [b] int32 (CUDA): valid
+        positions of each sequence; window (left, right): positions around the block that it
+        sees, -1 for all; sinks: first positions that stay visible. Without ws the scratch is
+        allocated for the call, so calls on several streams, and captured ones, do not share it."""
+        self._on(q, "q", torch.bfloat16, 4)
+        _need(q, "q")
+        self._on(cache.k, "cache")
+        d = self.kv4_attn_desc(q, cache, block_start, window, sinks, scale)
+        if kv_len is not None:
+            self._on(kv_len, "kv_len", torch.int32, 1)
+            _need(kv_len, "kv_len")
+            if kv_len.numel() != d.batch:
+                raise ValueError(f"kv_len has {kv_len.numel()} entries for {d.batch} sequences")
+        for t, name, dt, shape in ((out, "out", torch.bfloat16, q.shape),
+                                   (lse, "lse", torch.float32,
+                                    (d.batch, d.n_q_heads, d.block_len))):
+            if t is not None:
+                self._on(t, name, dt)
+                _need(t, name)
+                if tuple(t.shape) != tuple(shape):
+                    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if ws is not None:
+            self._on(ws, "ws")
+            _need(ws, "ws")
+        s = self._at(stream)
+        need = self.kv4_attention_workspace_bytes(d)
+        with self._memory_of(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None and want_lse:
+                lse = torch.empty((d.batch, d.n_q_heads, d.block_len), dtype=torch.float32,
+                                  device=q.device)
+            if ws is None:
+                ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        _check(load().fdl_kv4_attention(self._h, ctypes.byref(d), _ptr(q),
+                                        ctypes.byref(cache.buffers), _ptr(kv_len), _ptr(out),
+                                        _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+                                        _stream(s)))
+        return (out, lse) if (want_lse or lse is not None) else out
 
     # -- (b) LM head + confidence ----------------------------------------
     def lmhead_workspace_bytes(self, desc: LMHeadDesc) -> int:

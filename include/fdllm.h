@@ -42,7 +42,7 @@
 extern "C" {
 #endif
 
-#define FDL_ABI_VERSION 6
+#define FDL_ABI_VERSION 7
 
 #if defined(__GNUC__)
 #define FDL_API __attribute__((visibility("default")))
@@ -383,6 +383,99 @@ FDL_API int fdl_ffn(fdl_ctx* ctx, int rows, int hidden, int ffn, const float* no
 FDL_API int fdl_full_attention(fdl_ctx* ctx, const fdl_attn_desc* desc, const void* q,
                                const void* k_cache, const void* v_cache, void* out,
                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit K/V cache: rows quantised as they are written, read back, and the block
+ * attention over them. (A deployment form of the DualCache, for more sequences
+ * or longer ones in the same memory: 4.5 bits per value instead of 16.)
+ *
+ * Microscaled 4-bit floating point. Along head_dim every 16 values share one
+ * scale:
+ *   scale = e4m3(max |x| / 6)   8 bits, round to nearest even, at most 448
+ *   code  = e2m1(x / scale)     4 bits, round to nearest even, at most 6;
+ *                               0 where scale = 0
+ * and stand for code * scale, which bf16 holds exactly. e2m1 codes 0..7 are 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign. Values beyond 6 * 448 = 2688 and
+ * infinities saturate; a NaN makes its group's scale NaN (0x7f), and the whole
+ * group reads as NaN; groups whose largest value is at most 3 * 2^-9 read as 0.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void* k;        /* [b, Hkv, L, d/2] uint8: codes, the even dimension of a pair in the low nibble */
+    void* k_scale;  /* [b, Hkv, L, d/16] uint8: e4m3 scales */
+    void* v;        /* as k */
+    void* v_scale;  /* as k_scale */
+} fdl_kv4_cache;    /* device, every buffer 16-byte aligned, owned by the caller */
+
+typedef struct {
+    int batch;           /* b >= 1, at most 65535 */
+    int n_kv_heads;      /* Hkv >= 1 */
+    int head_dim;        /* d in {64, 128} */
+    int seq_len;         /* L >= 1 positions per (sequence, head) of the cache */
+    int dtype;           /* fdl_dtype of the unquantised rows */
+    int64_t seq_stride;  /* elements from a sequence, position or head of the unquantised */
+    int64_t row_stride;  /* rows to the next (>= 0, multiples of 16 bytes; d is contiguous), */
+    int64_t head_stride; /* so head-major rows serve too; all three 0: [b, n, Hkv, d] contiguous */
+} fdl_kv4_rows_desc;
+
+/* Quantise fresh rows into positions [start, start + n) of every sequence and
+ * head; all other positions are untouched (the 4-bit form of fdl_kv_store).
+ *   k_new, v_new [b, n, Hkv, d] dtype, device, 16-byte aligned, strides as in desc
+ * Errors: FDL_EINVAL (shape, range, null, alignment, strides), FDL_EUNSUPPORTED
+ * (head_dim; Hkv * n * d >= 2^33), FDL_ECUDA. */
+FDL_API int fdl_kv4_store(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const void* k_new,
+                          const void* v_new, int start, int n, const fdl_kv4_cache* cache,
+                          void* stream);
+
+/* Read positions [start, start + n) back: the values the cache stands for, in
+ * desc->dtype (exact in both types).
+ *   k_out, v_out [b, n, Hkv, d] dtype, device, 16-byte aligned, strides as in desc
+ *                (> 0 where there is more than one; rows must not overlap); either
+ *                may be NULL (not read)
+ * Errors: as fdl_kv4_store. */
+FDL_API int fdl_kv4_load(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const fdl_kv4_cache* cache,
+                         int start, int n, void* k_out, void* v_out, void* stream);
+
+typedef struct {
+    int batch;         /* as fdl_attn_desc ... */
+    int n_q_heads;
+    int n_kv_heads;
+    int head_dim;
+    int seq_len;
+    int block_start;
+    int block_len;
+    int dtype;         /* fdl_dtype of q and out: FDL_BF16 */
+    float scale;       /* softmax scale; 0 means 1/sqrt(head_dim) */
+    int window_left;   /* positions before the block that it sees; < 0: all */
+    int window_right;  /* positions after the block that it sees; < 0: all */
+    int sinks;         /* first positions of a sequence that stay visible, >= 0 */
+} fdl_kv4_attn_desc;
+
+/* Bytes of scratch fdl_kv4_attention needs for this shape on ctx's device (partial
+ * results where the positions are split over several blocks of threads). Returns
+ * 0 for an invalid context or descriptor. */
+FDL_API size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx,
+                                                 const fdl_kv4_attn_desc* desc);
+
+/* Block attention over a 4-bit cache (fdl_dualcache_attention's counterpart): for
+ * each sequence b, q-head h and block row i,
+ *   out[b,i,h,:] = sum_j softmax_j(scale * q[b,i,h,:] . K[b,g,j,:]) V[b,g,j,:]
+ * with K, V the values the cache stands for, g = h / (Hq/Hkv), over the positions
+ * j that the block sees: j < kv_len[b] (all L without kv_len), and
+ *   j < sinks  or  block_start - window_left <= j < block_start + block_len + window_right.
+ * The block slot's rows must be in the cache already (fdl_kv4_store). What a
+ * block does not see is not read into any result, whatever it holds. A sequence
+ * whose block sees nothing gets out = 0 and lse = -inf.
+ *   q       [b, B, Hq, d]  bf16, device, 16-byte aligned
+ *   kv_len  [b] int32, device, optional (NULL: L); clamped to [0, L]
+ *   out     [b, B, Hq, d]  bf16, device, 16-byte aligned (written; not q)
+ *   lse     [b, Hq, B] f32, device, optional: log sum_j exp(scale q.k_j)
+ *   ws      device scratch of >= fdl_kv4_attention_workspace_bytes(desc) bytes,
+ *           16-byte aligned; calls that may overlap on the GPU need one each
+ * Errors: FDL_EINVAL, FDL_EUNSUPPORTED (head_dim; q not bf16), FDL_EWORKSPACE,
+ * FDL_ECUDA. */
+FDL_API int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q,
+                              const fdl_kv4_cache* cache, const int32_t* kv_len, void* out,
+                              float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /* ---- the whole decode: DualCache block decoding with the threshold rule ----
  * Fast-dLLM (README "Key techniques" 1 and 2; aibase news "Innovations" 1

@@ -11,3 +11,4 @@ from .fastdllm import (attention, dualcache_attention, kv_store,  # noqa: F401
                        prefix_hidden, generate_dualcache, generate_prefixcache, generate_nocache,
                        generate_sequential, apply_rope, rms_norm, silu,
                        tau_as_single, Confidence, DecodeTrace)
+from .kv4 import kv4_attention, kv4_quantise, kv4_values, kv4_visible  # noqa: F401

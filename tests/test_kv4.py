@@ -1,0 +1,210 @@
+"""The 4-bit K/V cache without a GPU: the oracle's number formats, and the refusals of the
+library's entry points, which come before any device work."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from block_kv_cache_b200 import fdllm
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+EINVAL, EUNSUP, EWS = fdllm.FDL_EINVAL, fdllm.FDL_EUNSUPPORTED, fdllm.FDL_EWORKSPACE
+
+
+# ----------------------------------------------------------------- the oracle's formats
+def test_e4m3_table_is_torchs():
+    t = torch.arange(128, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    from oracle import kv4
+    np.testing.assert_array_equal(kv4.E4M3, t)
+
+
+def test_quantise_ties_and_limits():
+    def values(*x):
+        row = np.zeros(16)
+        row[:len(x)] = x
+        return O.kv4_values(*O.kv4_quantise(row))[:len(x)]
+    # scale 1 (max 6): every border of two codes goes to the even one
+    np.testing.assert_array_equal(
+        values(6, .25, .75, 1.25, 1.75, 2.5, 3.5, 5, -.25, -5),
+        [6, 0, 1, 1, 2, 2, 4, 4, 0, -4])
+    np.testing.assert_array_equal(values(6, .2501, .7499, 2.501, 5.001), [6, .5, .5, 3, 6])
+    np.testing.assert_array_equal(values(1e30, -1e30, 448.0), [2688, -2688, 448])
+    np.testing.assert_array_equal(values(np.inf, -np.inf, 1.0), [2688, -2688, 0])
+    # the scale of a largest value of 3 * 2^-9 is a tie between 0 and 2^-9
+    np.testing.assert_array_equal(values(3 * 2.0 ** -9, 2.0 ** -9), [0, 0])
+    assert values(3.01 * 2.0 ** -9)[0] == 3 * 2.0 ** -9
+    assert np.isnan(O.kv4_values(*O.kv4_quantise(np.array([np.nan] + [1.0] * 15)))).all()
+
+
+def test_quantise_against_scaled_search():
+    """Every value is the nearest product of a code and its group's scale."""
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((400, 32)) * 2.0 ** rng.integers(-6, 8, (400, 1))
+    codes, scales = O.kv4_quantise(x)
+    v = O.kv4_values(codes, scales)
+    from oracle import kv4
+    s = np.repeat(kv4.E4M3[scales], 16, -1)
+    grid = np.concatenate([-kv4.E2M1, kv4.E2M1])
+    best = np.abs(x[..., None] - grid * s[..., None]).min(-1)
+    np.testing.assert_array_equal(np.abs(x - v), best)
+
+
+def test_visible_positions():
+    v = O.kv4_visible(20, 8, 4, 18, (3, 2), 2)
+    assert np.flatnonzero(v).tolist() == [0, 1] + list(range(5, 14))
+    assert O.kv4_visible(20, 8, 4, 9, (3, 2), 2).sum() == 2 + 4
+    assert O.kv4_visible(20, 8, 4, 0).sum() == 0
+    assert O.kv4_visible(20, 8, 4).sum() == 20
+    assert np.flatnonzero(O.kv4_visible(20, 0, 1, None, (0, 0), 5)).tolist() == [0, 1, 2, 3, 4]
+
+
+# ------------------------------------------------------------------------ the binding
+def _header():
+    return open(os.path.join(ROOT, "include", "fdllm.h")).read()
+
+
+def test_structs_match_the_header():
+    sizes = {"int": 4, "float": 4, "int64_t": 8}
+    for cname, py in (("fdl_kv4_cache", fdllm.Kv4Buffers),
+                      ("fdl_kv4_rows_desc", fdllm.Kv4RowsDesc),
+                      ("fdl_kv4_attn_desc", fdllm.Kv4AttnDesc)):
+        src = _header()
+        end = re.search(r"\}\s*" + cname + r"\s*;", src).start()
+        body = re.sub(r"/\*.*?\*/", "", src[src.rindex("typedef struct {", 0, end):end]
+                      .split("{", 1)[1], flags=re.S)
+        fields = re.findall(r"([\w\s\*]+?)\s*\b(\w+);", body)
+        assert [f for _, f in fields] == [f for f, _ in py._fields_], cname
+        for (ctype, fname), (_, pytype) in zip(fields, py._fields_):
+            assert ctypes.sizeof(pytype) == (8 if "*" in ctype else sizes[ctype.strip()]), fname
+
+
+# ------------------------------------------------------------------- refusals, no device
+# A context is only looked into once every argument has passed: zeroed memory
+# stands in for one. Addresses are never followed.
+CTX = ctypes.create_string_buffer(4096)
+P = 1 << 20                                                  # an aligned "address"
+
+
+def ctx():
+    return ctypes.cast(CTX, ctypes.c_void_p)
+
+
+def cache(**kw):
+    b = fdllm.Kv4Buffers(P, P, P, P)
+    for k, v in kw.items():
+        setattr(b, k, v)
+    return ctypes.byref(b)
+
+
+def rows(**kw):
+    f = dict(batch=2, n_kv_heads=4, head_dim=128, seq_len=100, dtype=fdllm.FDL_BF16,
+             seq_stride=0, row_stride=0, head_stride=0)
+    f.update(kw)
+    return ctypes.byref(fdllm.Kv4RowsDesc(**f))
+
+
+BAD_ROWS = [
+    (dict(batch=0), EINVAL), (dict(batch=65536), EINVAL), (dict(n_kv_heads=0), EINVAL),
+    (dict(seq_len=0), EINVAL), (dict(head_dim=96), EUNSUP), (dict(head_dim=32), EUNSUP),
+    (dict(dtype=2), EINVAL), (dict(row_stride=-8), EINVAL),
+    (dict(row_stride=516, head_stride=128, seq_stride=51200), EINVAL),
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD_ROWS)
+def test_store_and_load_refuse_bad_descriptors(kw, code):
+    L = fdllm.load()
+    assert L.fdl_kv4_store(ctx(), rows(**kw), P, P, 0, 10, cache(), None) == code
+    assert L.fdl_kv4_load(ctx(), rows(**kw), cache(), 0, 10, P, P, None) == code
+    assert len(L.fdl_last_error()) > 0
+
+
+@pytest.mark.parametrize("start,n", [(0, 0), (0, -1), (-1, 5), (91, 10), (0, 101),
+                                     (2147483647, 1), (1, 2147483647)])
+def test_store_and_load_refuse_bad_ranges(start, n):
+    L = fdllm.load()
+    assert L.fdl_kv4_store(ctx(), rows(), P, P, start, n, cache(), None) == EINVAL
+    assert L.fdl_kv4_load(ctx(), rows(), cache(), start, n, P, P, None) == EINVAL
+
+
+def test_store_and_load_refuse_bad_buffers():
+    L = fdllm.load()
+    assert L.fdl_kv4_store(None, rows(), P, P, 0, 10, cache(), None) == EINVAL
+    assert L.fdl_kv4_store(ctx(), None, P, P, 0, 10, cache(), None) == EINVAL
+    assert L.fdl_kv4_store(ctx(), rows(), None, P, 0, 10, cache(), None) == EINVAL
+    assert L.fdl_kv4_store(ctx(), rows(), P, None, 0, 10, cache(), None) == EINVAL
+    assert L.fdl_kv4_store(ctx(), rows(), P + 8, P, 0, 10, cache(), None) == EINVAL
+    assert L.fdl_kv4_store(ctx(), rows(), P, P, 0, 10, None, None) == EINVAL
+    for f in ("k", "k_scale", "v", "v_scale"):
+        assert L.fdl_kv4_store(ctx(), rows(), P, P, 0, 10, cache(**{f: None}), None) == EINVAL
+        assert L.fdl_kv4_load(ctx(), rows(), cache(**{f: P + 4}), 0, 10, P, P, None) == EINVAL
+    assert L.fdl_kv4_load(ctx(), rows(), cache(), 0, 10, None, None, None) == EINVAL
+    assert L.fdl_kv4_load(ctx(), rows(), cache(), 0, 10, P + 2, P, None) == EINVAL
+    # rows written on top of one another
+    same = dict(head_stride=128, row_stride=0, seq_stride=5120)
+    assert L.fdl_kv4_load(ctx(), rows(**same), cache(), 0, 10, P, P, None) == EINVAL
+    # more rows than one call counts
+    big = dict(seq_len=1 << 30, n_kv_heads=64)
+    assert L.fdl_kv4_store(ctx(), rows(**big), P, P, 0, 1 << 30, cache(), None) == EUNSUP
+
+
+def attn(**kw):
+    f = dict(batch=2, n_q_heads=8, n_kv_heads=4, head_dim=128, seq_len=100, block_start=50,
+             block_len=32, dtype=fdllm.FDL_BF16, scale=0.0, window_left=-1, window_right=-1,
+             sinks=0)
+    f.update(kw)
+    return ctypes.byref(fdllm.Kv4AttnDesc(**f))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), EINVAL), (dict(n_q_heads=6), EINVAL), (dict(n_kv_heads=0), EINVAL),
+    (dict(head_dim=96), EUNSUP), (dict(dtype=fdllm.FDL_F32), EUNSUP), (dict(dtype=7), EINVAL),
+    (dict(block_len=0), EINVAL), (dict(block_len=129, seq_len=400), EINVAL),
+    (dict(block_start=-1), EINVAL), (dict(block_start=69), EINVAL),
+    (dict(block_start=2147483647), EINVAL), (dict(scale=-1.0), EINVAL),
+    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
+    (dict(sinks=-1), EINVAL), (dict(batch=1 << 22, n_q_heads=64), EUNSUP),
+])
+def test_attention_refuses_bad_descriptors(kw, code):
+    L = fdllm.load()
+    assert L.fdl_kv4_attention(ctx(), attn(**kw), P, cache(), None, 2 * P, None, P, 1 << 40,
+                               None) == code
+    assert L.fdl_kv4_attention_workspace_bytes(ctx(), attn(**kw)) == 0
+
+
+def test_attention_refuses_bad_buffers():
+    L = fdllm.load()
+
+    def call(c=None, d=None, q=P, ca=None, kv_len=None, out=2 * P, lse=None, ws=P, n=1 << 30):
+        return L.fdl_kv4_attention(c or ctx(), d or attn(), q, ca or cache(), kv_len, out, lse, ws,
+                                   n, None)
+    assert L.fdl_kv4_attention(None, attn(), P, cache(), None, 2 * P, None, P, 99, None) == EINVAL
+    assert L.fdl_kv4_attention(ctx(), None, P, cache(), None, 2 * P, None, P, 99, None) == EINVAL
+    assert L.fdl_kv4_attention(ctx(), attn(), P, None, None, 2 * P, None, P, 99, None) == EINVAL
+    assert call(q=None) == EINVAL
+    assert call(out=None) == EINVAL
+    assert call(out=P) == EINVAL                             # in place
+    assert call(q=P + 8) == EINVAL
+    assert call(out=2 * P + 8) == EINVAL
+    assert call(lse=P + 2) == EINVAL
+    assert call(kv_len=P + 1) == EINVAL
+    assert call(ca=cache(v_scale=None)) == EINVAL
+    assert call(ca=cache(k_scale=P + 8)) == EINVAL
+    assert call(ws=None) == EWS
+    assert call(ws=P + 4) == EWS
+    assert call(n=0) == EWS
+    assert L.fdl_kv4_attention_workspace_bytes(None, attn()) == 0
+    # widths beyond int: the window is clipped to the sequence, not wrapped
+    assert L.fdl_kv4_attention_workspace_bytes(
+        ctx(), attn(window_left=2147483647, window_right=2147483647, sinks=2147483647)) > 0
+
+
+def test_binding_refuses_cpu_tensors():
+    z = torch.zeros((1, 1, 4, 64), dtype=torch.uint8)
+    s = torch.zeros((1, 1, 4, 8), dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        fdllm.Kv4Cache(z, s, z, s)
