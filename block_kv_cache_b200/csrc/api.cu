@@ -169,7 +169,10 @@ int fdl_create(fdl_ctx** out, int device) {
     if (e == cudaSuccess) e = cudaMalloc(&c->d_sync, kSyncBytes);
     if (e == cudaSuccess) e = cudaMemset(c->d_sync, 0, kSyncBytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) fdl::attn_tc_warm();   // host-side queries, no launch
+    if (e == cudaSuccess) {                      // host-side queries, no launch
+        fdl::attn_tc_warm();
+        fdl::kv4_attention_warm();
+    }
     if (e != cudaSuccess) {
         if (c->d_err) cudaFree(c->d_err);
         if (c->d_acc) cudaFree(c->d_acc);
@@ -814,7 +817,8 @@ int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(FDL_ECUDA, "kv4_attention: cannot select device");
     const cudaError_t e = fdl::launch_kv4_attention(s, q, kv4_ptrs(cache), out, lse, ws,
-                                                    ctx->sm_count, (cudaStream_t)stream);
+                                                    ctx->sm_count, ctx->d_err,
+                                                    (cudaStream_t)stream);
     return e == cudaSuccess ? FDL_OK : cuda_fail(e, "kv4_attention launch");
 }
 

@@ -15,6 +15,22 @@ namespace fdl {
 
 constexpr int KV4_GROUP = 16;
 
+// Division by a fixed n of numbers below 2^31, by a multiplication with
+// ceil(2^(31+s) / n), 2^(s-1) < n <= 2^s (Granlund and Montgomery 1994).
+struct FastDiv {
+    uint32_t n, mul, sh;
+    FastDiv() : n(1), mul(0), sh(0) {}
+    explicit FastDiv(uint32_t d) : n(d), mul(0), sh(0) {
+        if (d > 1) {
+            while ((1ull << sh) < d) ++sh;
+            mul = (uint32_t)(((1ull << (31 + sh)) + d - 1) / d);
+        }
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t x) const {
+        return n == 1 ? x : __umulhi(x, mul) >> (sh - 1);
+    }
+};
+
 // e4m3 byte of |x| (x >= 0): round to nearest even, Inf -> 448, NaN -> 0x7f.
 __device__ __forceinline__ uint32_t e4m3_byte(float x) {
     uint16_t h;

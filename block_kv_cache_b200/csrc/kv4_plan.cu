@@ -1,0 +1,204 @@
+// Attention over the 4-bit K/V cache: which kernel, how many splits, and the
+// kernel that joins partial results.
+#include "kv4_attn.cuh"
+#include "timeline.cuh"
+
+namespace fdl {
+
+namespace {
+
+// The partial outputs of a row joined: one block per row of a unit, its warps
+// taking every 8th part and its lanes D / 32 columns each.
+constexpr int JOIN_WARPS = 8;
+
+template <int D>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const Kv4AttnArgs a) {
+    __shared__ float part[JOIN_WARPS][D];
+    __shared__ float sums[JOIN_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunk = blockIdx.x % a.chunks, u = blockIdx.x / a.chunks;
+    const int h = u % a.Hkv, bb = u / a.Hkv;
+    const int r = blockIdx.y, pr = chunk * a.chunk_rows + r;
+    if (threadIdx.x == 0) FDL_TL(0, 0);
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x == 0) FDL_TL(0, 1);
+    if (pr >= a.rows) return;
+    const size_t at = (size_t)blockIdx.x * a.parts * a.chunk_rows + r;
+    float M = -INFINITY;
+    for (int s = lane; s < a.parts; s += 32)
+        M = fmaxf(M, a.part_ml[at + (size_t)s * a.chunk_rows].x);
+    M = warp_max(M);
+    const float Ms = M == -INFINITY ? 0.f : M;
+    constexpr int E = D / 32;                // columns per lane
+    float acc[E], sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < E; ++x) acc[x] = 0.f;
+#pragma unroll 4
+    for (int s = warp; s < a.parts; s += JOIN_WARPS) {
+        const float2 p = a.part_ml[at + (size_t)s * a.chunk_rows];
+        const float f = ex2(p.x - Ms);
+        const float* src = a.part + (at + (size_t)s * a.chunk_rows) * D + lane * E;
+        sum += p.y * f;
+#pragma unroll
+        for (int x = 0; x < E; x += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(src + x);
+            acc[x] += v.x * f;
+            acc[x + 1] += v.y * f;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < E; ++x) part[warp][lane * E + x] = acc[x];
+    if (lane == 0) sums[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    float o0 = 0.f, o1 = 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+        o0 += part[w][2 * threadIdx.x];
+        o1 += part[w][2 * threadIdx.x + 1];
+        sum += sums[w];
+    }
+    const RowAt row(a, h, pr);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;              // nothing visible: 0
+    *reinterpret_cast<__nv_bfloat162*>(a.out + row.at(a, bb, D) + 2 * threadIdx.x) = __floats2bfloat162_rn(o0 * inv, o1 * inv);
+    if (a.lse && threadIdx.x == 0)
+        a.lse[row.lse(a, bb)] = kv4_lse(M, sum);
+    if (threadIdx.x == 0) FDL_TL(0, 2);
+}
+
+// The most positions that a sequence may see.
+int most_seen(const Kv4Attn& s) {
+    if (s.sinks >= s.win_lo) return s.sinks > s.win_hi ? s.sinks : s.win_hi;
+    return s.sinks + s.win_hi - s.win_lo;
+}
+
+#ifndef MANY_ROWS
+#define MANY_ROWS 32
+#endif
+
+Kv4Plan plan_of(const Kv4Attn& s, int sm_count) {
+    Kv4Plan p;
+    const int rows = s.block_len * (s.n_q_heads / s.n_kv_heads), seen = most_seen(s);
+    p.many = rows > MANY_ROWS;
+    if (p.many) {
+        p.chunks = (rows + 255) / 256;
+        p.chunk_rows = (rows + p.chunks - 1) / p.chunks;
+        p.mt = p.chunk_rows <= 128 ? 1 : 2;
+    } else {
+        p.mt = rows <= 16 ? 1 : 2;
+        p.chunks = (rows + 16 * p.mt - 1) / (16 * p.mt);
+        p.chunk_rows = (rows + p.chunks - 1) / p.chunks;
+    }
+    p.units = (long long)s.batch * s.n_kv_heads * p.chunks;
+    // as many splits as fill the GPU once, each of 64 (few rows) or 128 positions
+    const int slots = sm_count * (!p.many && p.mt == 1 ? 2 : 1), least = p.many ? 128 : 64;
+    long long n = p.units < slots ? slots / p.units : 1;
+    const long long most = (seen + least - 1) / least;
+    if (n > most) n = most;
+    if (n < 1) n = 1;
+    auto clusters = [&](int c) {
+        return p.many ? kv4_many_clusters(s.head_dim, p.mt, c)
+                      : kv4_few_clusters(s.head_dim, p.mt, c);
+    };
+    if (n > 8) {                 // clusters of 4 fill the GPU better than of 8
+        const long long fit = clusters(4) / p.units, want = n / 4;
+        p.cluster = 4;
+        p.n_splits = 4 * (int)(fit > 0 && fit < want ? fit : want);
+        return p;
+    }
+    // fewer while the clusters would not all be resident at once
+    for (; n > 1; --n) {
+        const int fit = clusters((int)n);
+        if (fit <= 0 || p.units <= fit) break;
+    }
+    p.cluster = p.n_splits = (int)n;
+    return p;
+}
+
+int parts_of(const Kv4Plan& p) { return p.n_splits / p.cluster; }
+
+}  // namespace
+
+int kv4_clusters(const void* kernel, int threads, size_t smem, int c, std::atomic<int>* known) {
+    const int n0 = known[c].load(std::memory_order_relaxed);
+    if (n0 > 0) return n0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = c;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[c].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+void kv4_attention_warm() {
+    for (int d = 64; d <= 128; d += 64)
+        for (int mt = 1; mt <= 2; ++mt)
+            for (int c = 2; c <= 8; ++c) {
+                (void)kv4_few_clusters(d, mt, c);
+                (void)kv4_many_clusters(d, mt, c);
+            }
+}
+
+size_t kv4_attention_workspace_bytes(const Kv4Attn& s, int sm_count) {
+    const Kv4Plan p = plan_of(s, sm_count);
+    if (parts_of(p) == 1) return 16;
+    return (size_t)p.units * parts_of(p) * p.chunk_rows * (s.head_dim * 4 + 8);
+}
+
+cudaError_t launch_kv4_attention(const Kv4Attn& s, const void* q, const Kv4Ptrs& c, void* out,
+                                 float* lse, void* ws, int sm_count, int* err, cudaStream_t st) {
+    const Kv4Plan p = plan_of(s, sm_count);
+    Kv4AttnArgs a{};
+    a.q = (const bf16*)q;
+    a.k = c.k;
+    a.ks = c.k_scale;
+    a.v = c.v;
+    a.vs = c.v_scale;
+    a.out = (bf16*)out;
+    a.lse = lse;
+    a.kv_len = s.kv_len;
+    a.B = s.block_len;
+    a.Hq = s.n_q_heads;
+    a.Hkv = s.n_kv_heads;
+    a.G = s.n_q_heads / s.n_kv_heads;
+    a.by_g = FastDiv((uint32_t)a.G);
+    a.L = s.seq_len;
+    a.rows = a.B * a.G;
+    a.chunks = p.chunks;
+    a.chunk_rows = p.chunk_rows;
+    a.n_splits = p.n_splits;
+    a.cluster = p.cluster;
+    a.parts = parts_of(p);
+    a.sinks = s.sinks;
+    a.win_lo = s.win_lo;
+    a.win_hi = s.win_hi;
+    a.scale_log2 = s.scale * 1.4426950408889634f;
+    a.err = err;
+    a.part = (float*)ws;
+    a.part_ml = (float2*)((float*)ws + (size_t)p.units * a.parts * a.chunk_rows * s.head_dim);
+    cudaError_t e = p.many ? launch_kv4_attn_many(a, p, s.head_dim, st)
+                           : launch_kv4_attn_few(a, p, s.head_dim, st);
+    if (e != cudaSuccess || a.parts == 1) return e;
+    const dim3 grid((unsigned)p.units, p.chunk_rows), block(32 * JOIN_WARPS);
+    return s.head_dim == 128 ? launch_pdl(kv4_join_kernel<128>, grid, block, 0, st, 0, a)
+                             : launch_pdl(kv4_join_kernel<64>, grid, block, 0, st, 0, a);
+}
+
+}  // namespace fdl
+
+FDL_TL_READER(fdl_timeline_kv4_join)

@@ -18,21 +18,6 @@ namespace {
 
 constexpr int KV4_THREADS = 256;
 
-// Division by a fixed n of numbers below 2^31, by a multiplication with
-// ceil(2^(31+s) / n), 2^(s-1) < n <= 2^s (Granlund and Montgomery 1994).
-struct FastDiv {
-    uint32_t n, mul, sh;
-    explicit FastDiv(uint32_t d) : n(d), mul(0), sh(0) {
-        if (d > 1) {
-            while ((1ull << sh) < d) ++sh;
-            mul = (uint32_t)(((1ull << (31 + sh)) + d - 1) / d);
-        }
-    }
-    __device__ __forceinline__ uint32_t div(uint32_t x) const {
-        return n == 1 ? x : __umulhi(x, mul) >> (sh - 1);
-    }
-};
-
 struct Kv4RowsArgs {
     const void *k_src, *v_src;   // store: the fresh rows
     void *k_dst, *v_dst;         // load: the rows read back (null: not wanted)

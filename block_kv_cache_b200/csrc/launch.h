@@ -90,9 +90,12 @@ struct Kv4Attn {
     float scale;                 // resolved (never 0)
     const int32_t* kv_len;
 };
+// Query the cluster capacities that the plans use (outside any stream capture).
+void kv4_attention_warm();
 size_t kv4_attention_workspace_bytes(const Kv4Attn& s, int sm_count);
 cudaError_t launch_kv4_attention(const Kv4Attn& s, const void* q, const Kv4Ptrs& c, void* out,
-                                 float* lse, void* ws, int sm_count, cudaStream_t st);
+                                 float* lse, void* ws, int sm_count, int* dev_err,
+                                 cudaStream_t st);
 
 struct LMShape { int rows, hidden, vocab; };
 size_t lmhead_workspace_bytes(const LMShape& s);
