@@ -810,7 +810,7 @@ int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q
         return fail(FDL_EINVAL, "kv4_attention: q and out must be 16-byte aligned, lse and "
                     "kv_len 4-byte aligned");
     const size_t need = fdl::kv4_attention_workspace_bytes(s, ctx->sm_count);
-    if (!ws || ws_bytes < need || !aligned16(ws))
+    if (need > 16 && (!ws || ws_bytes < need || !aligned16(ws)))
         return fail(FDL_EWORKSPACE, "kv4_attention: workspace needs %zu bytes (16-byte aligned), "
                     "got %zu", need, ws ? ws_bytes : (size_t)0);
     s.kv_len = kv_len;

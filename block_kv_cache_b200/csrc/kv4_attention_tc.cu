@@ -591,8 +591,8 @@ template <int D, int MT>
 cudaError_t run_m4(const Kv4AttnArgs& a, long long units, cudaStream_t st) {
     using S = M4<D, MT>;
     auto kfn = kv4_attn_tc_kernel<D, MT>;
-    const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               S::TOTAL);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = kv4_allow_smem(kfn, S::TOTAL, allowed);
     if (e != cudaSuccess) return e;
     return launch_pdl(kfn, dim3((unsigned)(units * a.n_splits)), dim3(M4_THREADS), S::TOTAL, st,
                       a.cluster, a);

@@ -139,6 +139,19 @@ cudaError_t launch_kv4_attn_few(const Kv4AttnArgs& a, const Kv4Plan& p, int head
                                 cudaStream_t st);
 cudaError_t launch_kv4_attn_many(const Kv4AttnArgs& a, const Kv4Plan& p, int head_dim,
                                  cudaStream_t st);
+// The kernel's shared memory limit, set once per device.
+template <typename K>
+cudaError_t kv4_allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Clusters of c blocks (2 to 8) that the GPU holds at once: a cluster must fit in
 // one GPC. Queried once, outside any stream capture (fdl_create); 0 while unknown.
 int kv4_clusters(const void* kernel, int threads, size_t smem, int c, std::atomic<int>* known);

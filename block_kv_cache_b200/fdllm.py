@@ -123,6 +123,9 @@ class GenerateOpts(ctypes.Structure):
 BATCHING = {"lockstep": 0, "compact": 1, "per_sequence": 2}
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 class FdlError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"fdllm error {code}: {msg}")
@@ -245,20 +248,25 @@ class Kv4Cache:
     zeroed: every position reads as 0 until it is stored)."""
 
     def __init__(self, k, k_scale, v, v_scale):
-        for t, n in ((k, "k"), (k_scale, "k_scale"), (v, "v"), (v_scale, "v_scale")):
-            _need(t, n, torch.uint8, 4)
-            if t.device != k.device:
-                raise ValueError(f"{n} is on {t.device}, k on {k.device}")
-        b, h, L, half = k.shape
-        if half not in (32, 64):
-            raise ValueError(f"Kv4Cache: k has {half} code bytes per row, not 32 or 64 "
-                             "(head_dim 64 or 128)")
-        if v.shape != k.shape or k_scale.shape != (b, h, L, half // 8) \
-                or v_scale.shape != k_scale.shape:
-            raise ValueError(f"Kv4Cache: shapes {tuple(k.shape)}, {tuple(k_scale.shape)}, "
-                             f"{tuple(v.shape)}, {tuple(v_scale.shape)} do not belong together")
+        try:
+            b, h, L, half = shape = k.shape
+            if half not in (32, 64):
+                raise ValueError
+        except (AttributeError, ValueError):
+            raise ValueError("Kv4Cache: k must be [b, Hkv, L, 32 or 64] code bytes (head_dim 64 "
+                             "or 128)") from None
+        scales, device = (b, h, L, half // 8), k.get_device()
+        for t, n, want in ((k, "k", shape), (k_scale, "k_scale", scales), (v, "v", shape),
+                           (v_scale, "v_scale", scales)):
+            if t.dtype is not torch.uint8 or device < 0 or t.get_device() != device \
+                    or not t.is_contiguous():
+                raise TypeError(f"Kv4Cache: {n} must be a contiguous uint8 CUDA tensor on k's "
+                                "device")
+            if t.shape != want:
+                raise ValueError(f"Kv4Cache: {n} has shape {tuple(t.shape)}, not {tuple(want)}")
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
         self.batch, self.n_kv_heads, self.seq_len, self.head_dim = b, h, L, 2 * half
+        self.device_index = device
         self.buffers = Kv4Buffers(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
                                   v_scale.data_ptr())
 
@@ -385,25 +393,35 @@ class Context:
                                    _stream(stream)))
 
     # -- 4-bit K/V cache ----------------------------------------------------
-    def _on(self, t, name, dtype=None, ndim=None):
-        """A CUDA tensor on this context's device (strides are looked at elsewhere)."""
+    # These calls are short on the GPU, so their host side is kept short too: one
+    # test of everything that is usually right, and the words only when it is not.
+    def _at(self, stream):
+        """The CUDA stream handle of a call: `stream`'s, or the current one of this device."""
+        return stream.cuda_stream if stream is not None \
+            else torch._C._cuda_getCurrentRawStream(self.device)
+
+    def _here(self, t, name, dtype, shape):
+        """Raise unless t is a contiguous `dtype` tensor of `shape` on this device."""
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.device.index != self.device:
+        if t.get_device() != self.device:
             raise ValueError(f"{name} is on {t.device}, the context on cuda:{self.device}")
-        if dtype is not None and t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if ndim is not None and t.dim() != ndim:
-            raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
-
-    def _at(self, stream):
-        """The stream of a call: `stream`, or the current one of this context's device."""
-        return stream if stream is not None else torch.cuda.current_stream(self.device)
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
     @staticmethod
     def _memory_of(stream):
         """Tensors allocated inside belong to the stream of the call that writes them."""
-        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+        return _NO_CONTEXT if stream is None else torch.cuda.stream(stream)
+
+    def _kv4_cache(self, cache):
+        if cache.device_index != self.device:
+            raise ValueError(f"the cache is on cuda:{cache.device_index}, the context on "
+                             f"cuda:{self.device}")
 
     def _kv4_rows(self, cache, k, v, n):
         """Descriptor of unquantised rows k, v (either may be None) [b, n, Hkv, d]."""
@@ -413,63 +431,73 @@ class Context:
         for t, name in ((k, "k"), (v, "v")):
             if t is None:
                 continue
-            self._on(t, name, one.dtype, 4)
-            if tuple(t.shape) != want:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not one.dtype:
+                raise TypeError(f"{name} rows must be a CUDA tensor, k's and v's of one dtype")
+            if t.get_device() != self.device:
+                raise ValueError(f"{name} rows are on {t.device}, the context on "
+                                 f"cuda:{self.device}")
+            if t.shape != want:
                 raise ValueError(f"{name} rows have shape {tuple(t.shape)}, not {want}")
-            if t.stride(3) != 1:
+            st = t.stride()
+            if st[3] != 1:
                 raise ValueError(f"{name} rows must be contiguous along head_dim")
-            # a dimension of one position has no stride of its own
-            full = (n * want[2] * want[3], want[2] * want[3], want[3])
-            st = tuple(s if size > 1 else f for s, size, f in zip(t.stride(), want, full))
             if strides is not None and st != strides:
                 raise ValueError("k and v rows must have the same strides")
             strides = st
-        if not any(strides):
+        # a dimension of one position has no stride of its own
+        full = (n * want[2] * want[3], want[2] * want[3], want[3])
+        if want[0] == 1 or n == 1 or want[2] == 1:
+            strides = [s if size > 1 else f for s, size, f in zip(strides, want, full)]
+        if not (strides[0] or strides[1] or strides[2]):
             raise ValueError("rows without any stride are not supported")
         return Kv4RowsDesc(cache.batch, cache.n_kv_heads, cache.head_dim, cache.seq_len,
-                           _dtype_code(one), *strides)
+                           _dtype_code(one), strides[0], strides[1], strides[2])
 
     def kv4_store(self, k_new, v_new, cache: Kv4Cache, start, stream=None):
         """Quantise rows k_new, v_new [b, n, Hkv, d] (bf16 or f32; any strides with head_dim
         contiguous, the same for both) into positions [start, start + n) of the cache."""
-        self._on(cache.k, "cache")
-        self._on(k_new, "k_new", None, 4)
-        self._on(v_new, "v_new", None, 4)
+        self._kv4_cache(cache)
+        if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4 or v_new is None:
+            raise ValueError("kv4_store: k_new and v_new must be [b, n, Hkv, d]")
         n = k_new.shape[1]
         d = self._kv4_rows(cache, k_new, v_new, n)
-        _check(load().fdl_kv4_store(self._h, ctypes.byref(d), _ptr(k_new), _ptr(v_new),
-                                    int(start), int(n), ctypes.byref(cache.buffers),
-                                    _stream(self._at(stream))))
+        rc = (_lib or load()).fdl_kv4_store(self._h, ctypes.byref(d), k_new.data_ptr(),
+                                            v_new.data_ptr(), int(start), n,
+                                            ctypes.byref(cache.buffers), self._at(stream))
+        if rc:
+            _check(rc)
 
     def kv4_load(self, cache: Kv4Cache, start=0, n=None, *, dtype=torch.bfloat16, k_out=None,
                  v_out=None, stream=None):
         """The values positions [start, start + n) of the cache stand for (n: to the end):
         (k, v) [b, n, Hkv, d], new tensors of `dtype` (bf16 or f32) or the given k_out and
         v_out (of one of them alone, only that one is read)."""
-        self._on(cache.k, "cache")
+        self._kv4_cache(cache)
         n = cache.seq_len - int(start) if n is None else int(n)
-        s = self._at(stream)
         if k_out is None and v_out is None:
             if n < 1:
                 raise ValueError(f"kv4_load: {n} rows")
-            shape = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
             with self._memory_of(stream):
-                k_out, v_out = (torch.empty(shape, dtype=dtype, device=cache.k.device)
-                                for _ in range(2))
+                k_out = cache.k.new_empty((cache.batch, n, cache.n_kv_heads, cache.head_dim),
+                                          dtype=dtype)
+                v_out = torch.empty_like(k_out)
         d = self._kv4_rows(cache, k_out, v_out, n)
-        _check(load().fdl_kv4_load(self._h, ctypes.byref(d), ctypes.byref(cache.buffers),
-                                   int(start), n, _ptr(k_out), _ptr(v_out), _stream(s)))
+        rc = (_lib or load()).fdl_kv4_load(
+            self._h, ctypes.byref(d), ctypes.byref(cache.buffers), int(start), n,
+            None if k_out is None else k_out.data_ptr(),
+            None if v_out is None else v_out.data_ptr(), self._at(stream))
+        if rc:
+            _check(rc)
         return k_out, v_out
 
     def kv4_attn_desc(self, q, cache: Kv4Cache, block_start, window=(-1, -1), sinks=0,
                       scale=0.0) -> Kv4AttnDesc:
         b, B, Hq, d = q.shape
-        if (b, d) != (cache.batch, cache.head_dim):
+        if b != cache.batch or d != cache.head_dim:
             raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.batch} sequences "
                              f"and head_dim {cache.head_dim}")
         return Kv4AttnDesc(b, Hq, cache.n_kv_heads, d, cache.seq_len, int(block_start), B,
-                           _dtype_code(q), float(scale), int(window[0]), int(window[1]),
-                           int(sinks))
+                           FDL_BF16, scale, window[0], window[1], sinks)
 
     def kv4_attention_workspace_bytes(self, desc: Kv4AttnDesc) -> int:
         return int(load().fdl_kv4_attention_workspace_bytes(self._h, ctypes.byref(desc)))
@@ -482,40 +510,43 @@ class Context:
         positions of each sequence; window (left, right): positions around the block that it
         sees, -1 for all; sinks: first positions that stay visible. Without ws the scratch is
         allocated for the call, so calls on several streams, and captured ones, do not share it."""
-        self._on(q, "q", torch.bfloat16, 4)
-        _need(q, "q")
-        self._on(cache.k, "cache")
+        self._kv4_cache(cache)
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("kv4_attention: q must be [b, B, Hq, d]")
+        if q.get_device() != self.device or q.dtype is not torch.bfloat16 \
+                or not q.is_contiguous():
+            self._here(q, "q", torch.bfloat16, q.shape)
         d = self.kv4_attn_desc(q, cache, block_start, window, sinks, scale)
         if kv_len is not None:
-            self._on(kv_len, "kv_len", torch.int32, 1)
-            _need(kv_len, "kv_len")
-            if kv_len.numel() != d.batch:
-                raise ValueError(f"kv_len has {kv_len.numel()} entries for {d.batch} sequences")
-        for t, name, dt, shape in ((out, "out", torch.bfloat16, q.shape),
-                                   (lse, "lse", torch.float32,
-                                    (d.batch, d.n_q_heads, d.block_len))):
-            if t is not None:
-                self._on(t, name, dt)
-                _need(t, name)
-                if tuple(t.shape) != tuple(shape):
-                    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+            self._here(kv_len, "kv_len", torch.int32, (d.batch,))
+        if out is not None:
+            self._here(out, "out", torch.bfloat16, q.shape)
+        if lse is not None:
+            self._here(lse, "lse", torch.float32, (d.batch, d.n_q_heads, d.block_len))
         if ws is not None:
-            self._on(ws, "ws")
-            _need(ws, "ws")
-        s = self._at(stream)
-        need = self.kv4_attention_workspace_bytes(d)
-        with self._memory_of(stream):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None and want_lse:
-                lse = torch.empty((d.batch, d.n_q_heads, d.block_len), dtype=torch.float32,
-                                  device=q.device)
-            if ws is None:
-                ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        _check(load().fdl_kv4_attention(self._h, ctypes.byref(d), _ptr(q),
-                                        ctypes.byref(cache.buffers), _ptr(kv_len), _ptr(out),
-                                        _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
-                                        _stream(s)))
+            self._here(ws, "ws", ws.dtype, ws.shape)
+        if out is None or (lse is None and want_lse):
+            with self._memory_of(stream):
+                if out is None:
+                    out = torch.empty_like(q)
+                if lse is None and want_lse:
+                    lse = q.new_empty((d.batch, d.n_q_heads, d.block_len), dtype=torch.float32)
+        args = (self._h, ctypes.byref(d), q.data_ptr(), ctypes.byref(cache.buffers),
+                None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
+                None if lse is None else lse.data_ptr())
+        L = _lib or load()
+        if ws is None:
+            # most shapes need no scratch and say so by taking none
+            rc = L.fdl_kv4_attention(*args, None, 0, self._at(stream))
+            if rc == FDL_EWORKSPACE:
+                with self._memory_of(stream):
+                    ws = torch.empty(self.kv4_attention_workspace_bytes(d), dtype=torch.uint8,
+                                     device=q.device)
+        if ws is not None:
+            rc = L.fdl_kv4_attention(*args, ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     self._at(stream))
+        if rc:
+            _check(rc)
         return (out, lse) if (want_lse or lse is not None) else out
 
     # -- (b) LM head + confidence ----------------------------------------

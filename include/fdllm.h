@@ -451,7 +451,7 @@ typedef struct {
 } fdl_kv4_attn_desc;
 
 /* Bytes of scratch fdl_kv4_attention needs for this shape on ctx's device (partial
- * results where the positions are split over several blocks of threads). Returns
+ * results of a long sequence's splits); 16 means none: ws may then be NULL. Returns
  * 0 for an invalid context or descriptor. */
 FDL_API size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx,
                                                  const fdl_kv4_attn_desc* desc);
@@ -470,7 +470,8 @@ FDL_API size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx,
  *   out     [b, B, Hq, d]  bf16, device, 16-byte aligned (written; not q)
  *   lse     [b, Hq, B] f32, device, optional: log sum_j exp(scale q.k_j)
  *   ws      device scratch of >= fdl_kv4_attention_workspace_bytes(desc) bytes,
- *           16-byte aligned; calls that may overlap on the GPU need one each
+ *           16-byte aligned (NULL where that is 16); calls that may overlap on the
+ *           GPU need one each
  * Errors: FDL_EINVAL, FDL_EUNSUPPORTED (head_dim; q not bf16), FDL_EWORKSPACE,
  * FDL_ECUDA. */
 FDL_API int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q,

@@ -495,6 +495,8 @@ def test_binding_refusals(ctx):
     with pytest.raises(ValueError):
         ctx.kv4_store(k, k.transpose(0, 1).contiguous().transpose(0, 1), c, 0)   # other strides
     with pytest.raises(ValueError):
+        ctx.kv4_store(k, None, c, 0)
+    with pytest.raises(ValueError):
         ctx.kv4_store(k[..., :64], k[..., :64], c, 0)
     with pytest.raises(TypeError):
         ctx.kv4_store(k, k.float(), c, 0)

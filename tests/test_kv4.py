@@ -86,6 +86,7 @@ def test_structs_match_the_header():
 # A context is only looked into once every argument has passed: zeroed memory
 # stands in for one. Addresses are never followed.
 CTX = ctypes.create_string_buffer(4096)
+ctypes.cast(CTX, ctypes.POINTER(ctypes.c_int))[1] = 148      # its SM count
 P = 1 << 20                                                  # an aligned "address"
 
 
@@ -194,9 +195,14 @@ def test_attention_refuses_bad_buffers():
     assert call(kv_len=P + 1) == EINVAL
     assert call(ca=cache(v_scale=None)) == EINVAL
     assert call(ca=cache(k_scale=P + 8)) == EINVAL
-    assert call(ws=None) == EWS
-    assert call(ws=P + 4) == EWS
-    assert call(n=0) == EWS
+    # one token of a long sequence: split widely, with partial results
+    long = attn(batch=1, seq_len=1 << 20, block_len=1)
+    need = L.fdl_kv4_attention_workspace_bytes(ctx(), long)
+    assert need > 16
+    assert call(d=long, ws=None) == EWS
+    assert call(d=long, ws=P + 4) == EWS
+    assert call(d=long, n=need - 1) == EWS
+    assert L.fdl_kv4_attention_workspace_bytes(ctx(), attn()) == 16      # none, and none asked for
     assert L.fdl_kv4_attention_workspace_bytes(None, attn()) == 0
     # widths beyond int: the window is clipped to the sequence, not wrapped
     assert L.fdl_kv4_attention_workspace_bytes(
