@@ -699,10 +699,9 @@ int kv4_rows(const char* who, const fdl_ctx* ctx, const fdl_kv4_rows_desc* d, in
     if (n < 1 || start < 0 || (int64_t)start + n > d->seq_len)
         return fail(FDL_EINVAL, "%s: rows [%d, %lld) outside [0, %d)", who, start,
                     (long long)start + n, d->seq_len);
-    // the kernels count the 16-byte pieces of a sequence's rows in 31 bits
-    if ((int64_t)d->n_kv_heads * n * d->head_dim >= ((int64_t)1 << 33))
-        return fail(FDL_EUNSUPPORTED, "%s: %d heads x %d rows are too many for one call", who,
-                    d->n_kv_heads, n);
+    if (d->n_kv_heads > 32767)   // two grid rows per head
+        return fail(FDL_EUNSUPPORTED, "%s: %d heads are too many for one call", who,
+                    d->n_kv_heads);
     fdl::Kv4Rows r{d->batch, d->n_kv_heads, d->head_dim, d->seq_len, start, n,
                    d->dtype == FDL_BF16 ? 1 : 0, d->seq_stride, d->row_stride, d->head_stride};
     if (!r.seq_stride && !r.row_stride && !r.head_stride) {

@@ -88,6 +88,17 @@ __device__ __forceinline__ void e2m1x4_half2(uint16_t w, uint32_t* h) {
         : "h"(w));
 }
 
+// The larger magnitudes of two bf16 pairs; NaN wins.
+__device__ __forceinline__ uint32_t bf16x2_max_abs(uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+    return r;
+}
+// ... of both halves, as float bits.
+__device__ __forceinline__ uint32_t bf16x2_max_bits(uint32_t m) {
+    return max(m << 16, m & 0xffff0000u);
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a),
                               *reinterpret_cast<const __half2*>(&b));

@@ -94,17 +94,6 @@ struct RowAt {
     }
 };
 
-// The larger magnitudes of two bf16 pairs; NaN wins.
-__device__ __forceinline__ uint32_t bf16x2_max_abs(uint32_t m, uint32_t x) {
-    uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
-    return r;
-}
-// ... of both halves, as float bits.
-__device__ __forceinline__ uint32_t bf16x2_max_bits(uint32_t m) {
-    return max(m << 16, m & 0xffff0000u);
-}
-
 // The power of two that puts a row's largest magnitude (as float bits) into
 // [2^14, 2^15), and its inverse; 1 for a row of zeros, Inf or NaN.
 __device__ __forceinline__ void kv4_row_scale(uint32_t max_bits, float* f, float* inv) {

@@ -2,12 +2,16 @@
 //
 // Both are one pass over the data, bound by HBM at large sizes and by the
 // launch at a block's 32 rows: the store reads d * esize bytes per row and
-// writes d/2 + d/16, the load the reverse. A thread handles 16 bytes of the
-// unquantised row (8 bf16 or 4 f32 values), so 2 or 4 neighbouring lanes share
-// a group and combine their maxima by shuffles, and every access of a warp is
-// contiguous. The position is the fastest index after the row's pieces: the
-// cache rows of one (sequence, head) are contiguous, and partial sectors (8 or
-// 4 scale bytes per row) are filled by one warp.
+// writes d/2 + d/16, the load the reverse. A thread of the store has a group of
+// 16 values, so a scale is found once; a thread of the load has 16 bytes of the
+// row that it writes. A block lies within one sequence and covers whole heads or
+// a piece of one, so a thread's addresses come from one multiplication and
+// constant steps. Both are near their instruction limit, too: with half a group
+// per thread (its scale found twice) the store issued 128 instructions for 8
+// values, 83 % of the slots, and with a flat index divided for every access it
+// took 23.8 us and the load 16.8 for 32 sequences of 4 x 1024 rows of 128 bf16
+// (86 MB each way); now 14.9 and 14.6 us, 5.8 and 5.9 TB/s, 0.89 and 0.90 of the
+// measured HBM rate. A block of 32 rows of 32 heads takes 1.6 us either way.
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.h"
@@ -17,6 +21,7 @@ namespace fdl {
 namespace {
 
 constexpr int KV4_THREADS = 256;
+constexpr int LOAD_UNROLL = 4;                   // pieces per thread of the load
 
 struct Kv4RowsArgs {
     const void *k_src, *v_src;   // store: the fresh rows
@@ -24,42 +29,66 @@ struct Kv4RowsArgs {
     Kv4Ptrs c;
     long long seq_stride, row_stride, head_stride;   // of the rows, in elements
     int heads, L, start, n;
-    uint32_t items;              // per sequence: heads * n * pieces of a row
-    FastDiv by_n;
+    int head_blocks;             // blocks along the heads (grid.y is twice that: K, then V)
 };
 
 template <typename T> struct Piece { static constexpr int N = 16 / sizeof(T); };
 
-__device__ __forceinline__ void unpack(const uint4& w, float (&v)[8]) {     // 8 bf16
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// A group of 16 values as loaded: 2 (bf16) or 4 (f32) 16-byte words.
+template <typename T> struct Group { uint4 w[sizeof(T)]; };
+
+// Largest |x| of a group as float bits; NaN is above everything.
+__device__ __forceinline__ uint32_t max_bits(const Group<bf16>& g) {
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    for (int i = 0; i < 2; ++i) {
+        m = bf16x2_max_abs(bf16x2_max_abs(m, g.w[i].x), g.w[i].y);
+        m = bf16x2_max_abs(bf16x2_max_abs(m, g.w[i].z), g.w[i].w);
     }
+    return bf16x2_max_bits(m);
 }
-__device__ __forceinline__ void unpack(const uint4& w, float (&v)[4]) {     // 4 f32
-    v[0] = __uint_as_float(w.x);
-    v[1] = __uint_as_float(w.y);
-    v[2] = __uint_as_float(w.z);
-    v[3] = __uint_as_float(w.w);
+__device__ __forceinline__ uint32_t max_bits(const Group<float>& g) {
+    uint32_t m = 0;
+    const uint32_t a = 0x7fffffffu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = max(m, max(max(g.w[i].x & a, g.w[i].y & a), max(g.w[i].z & a, g.w[i].w & a)));
+    return m;
 }
 
-// Quantise the N values of this lane, whose group of 16 lies in 16 / N
-// neighbouring lanes (all of which call this); returns the codes, *scale the byte.
-template <int N>
-__device__ __forceinline__ uint32_t quantise(float (&v)[N], uint32_t* scale) {
-    // the maximum of |x| as unsigned bits, which orders NaN above everything
-    uint32_t mb = 0;
+__device__ __forceinline__ void unpack(const Group<bf16>& g, float (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) mb = max(mb, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t u[4] = {g.w[i].x, g.w[i].y, g.w[i].z, g.w[i].w};
 #pragma unroll
-    for (int o = 1; o < KV4_GROUP / N; o <<= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+        for (int y = 0; y < 4; ++y) {
+            v[8 * i + 2 * y] = __uint_as_float(u[y] << 16);
+            v[8 * i + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
+        }
+    }
+}
+__device__ __forceinline__ void unpack(const Group<float>& g, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[4 * i] = __uint_as_float(g.w[i].x);
+        v[4 * i + 1] = __uint_as_float(g.w[i].y);
+        v[4 * i + 2] = __uint_as_float(g.w[i].z);
+        v[4 * i + 3] = __uint_as_float(g.w[i].w);
+    }
+}
+
+// The codes of a group, and its scale byte.
+template <typename T>
+__device__ __forceinline__ uint2 quantise(const Group<T>& g, uint32_t* scale) {
+    float v[16];
+    unpack(g, v);
+    const uint32_t mb = max_bits(g);
     // max / 6 and x / scale as products with a reciprocal held in two floats
     // (fma(x, hi, x * lo), after Brisebarre and Muller): a quotient on the
     // border of two codes stays on it, where a single reciprocal's rounding
-    // error moved 162 of the bf16 ties to the wrong side. A quotient next to
-    // a border differs from it by more than its rounding.
+    // error moved 162 of the bf16 ties to the wrong side (and for three of the
+    // eight significands of a scale no single one keeps them all). A quotient
+    // next to a border differs from it by more than its rounding.
     const float mx = __uint_as_float(mb);
     constexpr float sixth_hi = 1.f / 6.f;
     constexpr float sixth_lo = (float)(1.0 / 6.0 - (double)sixth_hi);
@@ -67,149 +96,128 @@ __device__ __forceinline__ uint32_t quantise(float (&v)[N], uint32_t* scale) {
     if (mb >= 0x7f800000u) {                     // Inf saturates, NaN marks its group
         q = mx;
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = fminf(fmaxf(v[i], -3.4e38f), 3.4e38f);
+        for (int i = 0; i < 16; ++i) v[i] = fminf(fmaxf(v[i], -3.4e38f), 3.4e38f);
     }
     *scale = e4m3_byte(q);
     const float s = e4m3_f32(*scale);
     float hi = 0.f, lo = 0.f;
     if (s > 0.f) {
-        hi = __frcp_rn(s);
-        lo = fmaf(-s, hi, 1.f) * hi;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(s));
+        lo = fmaf(-s, hi, 1.f) * hi;             // what hi lacks
     }
-    float r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = i < N ? fmaf(v[i < N ? i : 0], hi, v[i < N ? i : 0] * lo) : 0.f;
-    return e2m1x8(r);
+    for (int i = 0; i < 16; ++i) v[i] = fmaf(v[i], hi, v[i] * lo);
+    return make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
 
-// Where item e of sequence bb lies: its row's cache index, its offset among the
-// unquantised rows (elements) and its piece of the row.
+// Where a thread works: blockDim = (pieces of a head at a time, heads at a time).
 template <int D, int N>
 struct Place {
-    size_t row;
-    long long at;
+    static constexpr int P = D / N;              // pieces of a row
+    bool is_v, head_ok;
+    int i, step, n;                              // first row, rows to the next piece, rows in all
     uint32_t piece;
-    __device__ __forceinline__ Place(const Kv4RowsArgs& a, int bb, uint32_t e) {
-        constexpr uint32_t P = D / N;
-        piece = e % P;
-        const uint32_t hr = e / P, h = a.by_n.div(hr), i = hr - h * (uint32_t)a.n;
+    size_t row;                                  // cache row of the first
+    long long at;                                // its piece's offset among the unquantised rows
+    __device__ __forceinline__ Place(const Kv4RowsArgs& a, int unroll) {
+        is_v = blockIdx.y >= (unsigned)a.head_blocks;
+        const int h = (int)(blockIdx.y - (is_v ? a.head_blocks : 0)) * blockDim.y + threadIdx.y;
+        const int bb = blockIdx.z;
+        head_ok = h < a.heads;
+        piece = threadIdx.x % P;
+        step = blockDim.x / P;
+        i = (int)blockIdx.x * step * unroll + threadIdx.x / P;
+        n = a.n;
         row = ((size_t)bb * a.heads + h) * a.L + a.start + i;
-        at = bb * a.seq_stride + i * a.row_stride + h * a.head_stride + piece * N;
+        at = bb * a.seq_stride + (long long)h * a.head_stride + (long long)i * a.row_stride +
+             piece * N;
     }
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(KV4_THREADS)
 kv4_store_kernel(const Kv4RowsArgs a) {
-    constexpr int N = Piece<T>::N, U = 2;
-    constexpr int LANES = KV4_GROUP / N;         // lanes of a group
     pdl_wait();
     pdl_trigger();
-    const bool is_v = blockIdx.y != 0;
-    const int bb = blockIdx.z;
-    const T* src = reinterpret_cast<const T*>(is_v ? a.v_src : a.k_src);
-    uint8_t* all_codes = is_v ? a.c.v : a.c.k;
-    uint8_t* all_scales = is_v ? a.c.v_scale : a.c.k_scale;
-    // items is a multiple of LANES and of the pieces of a row: a group's lanes
-    // are in range together, and the loop's bound below is uniform in a warp
-    const uint32_t base = blockIdx.x * (KV4_THREADS * U) + (threadIdx.x & ~31u) * U +
-                          (threadIdx.x & 31u);
-    uint4 w[U];
+    const Place<D, KV4_GROUP> p(a, 1);
+    if (!p.head_ok || p.i >= p.n) return;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        reinterpret_cast<const T*>(p.is_v ? a.v_src : a.k_src) + p.at);
+    Group<T> g;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t e = base + u * 32;
-        w[u] = make_uint4(0, 0, 0, 0);
-        if (e < a.items) {
-            const Place<D, N> p(a, bb, e);
-            w[u] = __ldcs(reinterpret_cast<const uint4*>(src + p.at));
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t e = base + u * 32;
-        float v[N];
-        unpack(w[u], v);
-        uint32_t sc;
-        const uint32_t codes = quantise<N>(v, &sc);
-        if (e >= a.items) continue;
-        const Place<D, N> p(a, bb, e);
-        uint8_t* c = all_codes + p.row * (D / 2) + p.piece * (N / 2);
-        if (N == 8) *reinterpret_cast<uint32_t*>(c) = codes;
-        else *reinterpret_cast<uint16_t*>(c) = (uint16_t)codes;
-        if (p.piece % LANES == 0)
-            all_scales[p.row * (D / KV4_GROUP) + p.piece / LANES] = (uint8_t)sc;
-    }
+    for (int i = 0; i < (int)sizeof(T); ++i) g.w[i] = __ldcs(src + i);
+    uint32_t sc;
+    const uint2 c = quantise<T>(g, &sc);
+    reinterpret_cast<uint2*>(p.is_v ? a.c.v : a.c.k)[p.row * (D / KV4_GROUP) + p.piece] = c;
+    (p.is_v ? a.c.v_scale : a.c.k_scale)[p.row * (D / KV4_GROUP) + p.piece] = (uint8_t)sc;
 }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(KV4_THREADS)
 kv4_load_kernel(const Kv4RowsArgs a) {
-    constexpr int N = Piece<T>::N, U = 4;
+    constexpr int N = Piece<T>::N, U = LOAD_UNROLL;
     constexpr int LANES = KV4_GROUP / N;
     pdl_wait();
     pdl_trigger();
-    const bool is_v = blockIdx.y != 0;
-    const int bb = blockIdx.z;
-    T* dst = reinterpret_cast<T*>(is_v ? a.v_dst : a.k_dst);
-    const uint8_t* all_codes = is_v ? a.c.v : a.c.k;
-    const uint8_t* all_scales = is_v ? a.c.v_scale : a.c.k_scale;
-    if (!dst) return;
-    const uint32_t base = blockIdx.x * (KV4_THREADS * U) + (threadIdx.x & ~31u) * U +
-                          (threadIdx.x & 31u);
+    const Place<D, N> p(a, U);
+    T* dst = reinterpret_cast<T*>(p.is_v ? a.v_dst : a.k_dst);
+    if (!dst || !p.head_ok) return;
+    dst += p.at;
+    const uint8_t* codes = (p.is_v ? a.c.v : a.c.k) + p.row * (D / 2) + p.piece * (N / 2);
+    const uint8_t* scales = (p.is_v ? a.c.v_scale : a.c.k_scale) + p.row * (D / KV4_GROUP) +
+                            p.piece / LANES;
     uint32_t w[U], sc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const uint32_t e = base + u * 32;
         w[u] = sc[u] = 0;
-        if (e < a.items) {
-            const Place<D, N> p(a, bb, e);
-            const uint8_t* c = all_codes + p.row * (D / 2) + p.piece * (N / 2);
+        if (p.i + u * p.step < p.n) {
+            const uint8_t* c = codes + (size_t)(u * p.step) * (D / 2);
             w[u] = N == 8 ? *reinterpret_cast<const uint32_t*>(c)
                           : *reinterpret_cast<const uint16_t*>(c);
-            sc[u] = all_scales[p.row * (D / KV4_GROUP) + p.piece / LANES];
+            sc[u] = scales[(size_t)(u * p.step) * (D / KV4_GROUP)];
         }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const uint32_t e = base + u * 32;
-        if (e >= a.items) continue;
-        const Place<D, N> p(a, bb, e);
-        uint32_t h[N / 2];
+        if (p.i + u * p.step >= p.n) break;
+        // code * scale is exact in f16, and then in T
+        const uint32_t s2 = e4m3x2_half2(sc[u] * 0x0101u);
+        uint32_t h[N / 2], o[4];
         if constexpr (N == 8) e2m1x8_half2(w[u], h);
         else e2m1x4_half2((uint16_t)w[u], h);
-        const float s = e4m3_f32(sc[u]);
-        float v[N];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-            v[2 * i] = f.x * s;                  // at most 6 significant bits: exact
-            v[2 * i + 1] = f.y * s;
-        }
-        uint4 o;
-        if constexpr (N == 8) {
-            uint32_t b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                b[i] = *reinterpret_cast<const uint32_t*>(&t);
+            const uint32_t v = hmul2(h[i], s2);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+            if constexpr (N == 8) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
+                o[i] = *reinterpret_cast<const uint32_t*>(&t);
+            } else {
+                o[2 * i] = __float_as_uint(f.x);
+                o[2 * i + 1] = __float_as_uint(f.y);
             }
-            o = make_uint4(b[0], b[1], b[2], b[3]);
-        } else {
-            o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                           __float_as_uint(v[3]));
         }
-        *reinterpret_cast<uint4*>(dst + p.at) = o;
+        // streamed: 3.5 times the bytes read (19 MB to 67 MB: 14.6 us, without 16.6)
+        __stcs(reinterpret_cast<uint4*>(dst + (long long)u * p.step * a.row_stride),
+               make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
 template <bool STORE>
 cudaError_t launch_rows(const Kv4Rows& s, const void* k_src, const void* v_src, void* k_dst,
                         void* v_dst, const Kv4Ptrs& c, cudaStream_t st) {
-    const int piece = s.bf16 ? 8 : 4, per_block = KV4_THREADS * (STORE ? 2 : 4);
-    const uint32_t items = (uint32_t)s.heads * s.n * (s.head_dim / piece);
+    const int pieces = s.head_dim / (STORE ? KV4_GROUP : s.bf16 ? 8 : 4),
+              unroll = STORE ? 1 : LOAD_UNROLL;
+    // as many pieces of a head as there are, up to a block; the rest of the block
+    // takes further heads
+    const long long items = (long long)s.n * pieces;
+    int x = KV4_THREADS;
+    while (x > 32 && x / 2 * (long long)unroll >= items) x /= 2;
+    const int y = KV4_THREADS / x, head_blocks = (s.heads + y - 1) / y;
+    const long long rows = (long long)x / pieces * unroll;
     Kv4RowsArgs a{k_src, v_src, k_dst, v_dst, c,
                   s.seq_stride, s.row_stride, s.head_stride,
-                  s.heads, s.seq_len, s.start, s.n, items, FastDiv((uint32_t)s.n)};
+                  s.heads, s.seq_len, s.start, s.n, head_blocks};
     void (*kfn)(const Kv4RowsArgs);
     if constexpr (STORE)
         kfn = s.bf16 ? (s.head_dim == 128 ? kv4_store_kernel<bf16, 128> : kv4_store_kernel<bf16, 64>)
@@ -219,8 +227,8 @@ cudaError_t launch_rows(const Kv4Rows& s, const void* k_src, const void* v_src, 
         kfn = s.bf16 ? (s.head_dim == 128 ? kv4_load_kernel<bf16, 128> : kv4_load_kernel<bf16, 64>)
                      : (s.head_dim == 128 ? kv4_load_kernel<float, 128>
                                           : kv4_load_kernel<float, 64>);
-    const dim3 grid((items + per_block - 1) / per_block, 2, s.batch);
-    return launch_pdl(kfn, grid, dim3(KV4_THREADS), 0, st, 0, a);
+    const dim3 grid((unsigned)((s.n + rows - 1) / rows), 2 * head_blocks, s.batch);
+    return launch_pdl(kfn, grid, dim3(x, y), 0, st, 0, a);
 }
 
 }  // namespace

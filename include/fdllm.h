@@ -421,7 +421,7 @@ typedef struct {
  * head; all other positions are untouched (the 4-bit form of fdl_kv_store).
  *   k_new, v_new [b, n, Hkv, d] dtype, device, 16-byte aligned, strides as in desc
  * Errors: FDL_EINVAL (shape, range, null, alignment, strides), FDL_EUNSUPPORTED
- * (head_dim; Hkv * n * d >= 2^33), FDL_ECUDA. */
+ * (head_dim; more than 32767 heads), FDL_ECUDA. */
 FDL_API int fdl_kv4_store(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const void* k_new,
                           const void* v_new, int start, int n, const fdl_kv4_cache* cache,
                           void* stream);

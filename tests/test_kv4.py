@@ -148,9 +148,8 @@ def test_store_and_load_refuse_bad_buffers():
     # rows written on top of one another
     same = dict(head_stride=128, row_stride=0, seq_stride=5120)
     assert L.fdl_kv4_load(ctx(), rows(**same), cache(), 0, 10, P, P, None) == EINVAL
-    # more rows than one call counts
-    big = dict(seq_len=1 << 30, n_kv_heads=64)
-    assert L.fdl_kv4_store(ctx(), rows(**big), P, P, 0, 1 << 30, cache(), None) == EUNSUP
+    # more heads than one call's grid holds
+    assert L.fdl_kv4_store(ctx(), rows(n_kv_heads=32768), P, P, 0, 9, cache(), None) == EUNSUP
 
 
 def attn(**kw):
