@@ -10,8 +10,8 @@
 // per thread (its scale found twice) the store issued 128 instructions for 8
 // values, 83 % of the slots, and with a flat index divided for every access it
 // took 23.8 us and the load 16.8 for 32 sequences of 4 x 1024 rows of 128 bf16
-// (86 MB each way); now 14.9 and 14.6 us, 5.8 and 5.9 TB/s, 0.89 and 0.90 of the
-// measured HBM rate. A block of 32 rows of 32 heads takes 1.6 us either way.
+// (86 MB each way); now 14.8 and 14.7 us, 5.8 TB/s, 0.89 of the measured HBM rate. A block of
+// 32 rows of 32 heads takes 1.6 us either way.
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.h"
@@ -137,19 +137,31 @@ struct Place {
 template <typename T, int D>
 __global__ void __launch_bounds__(KV4_THREADS)
 kv4_store_kernel(const Kv4RowsArgs a) {
+    constexpr int U = 4 / sizeof(T);             // 64 bytes of rows per thread
     pdl_wait();
     pdl_trigger();
-    const Place<D, KV4_GROUP> p(a, 1);
-    if (!p.head_ok || p.i >= p.n) return;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        reinterpret_cast<const T*>(p.is_v ? a.v_src : a.k_src) + p.at);
-    Group<T> g;
+    const Place<D, KV4_GROUP> p(a, U);
+    if (!p.head_ok) return;
+    const T* src = reinterpret_cast<const T*>(p.is_v ? a.v_src : a.k_src) + p.at;
+    uint2* codes = reinterpret_cast<uint2*>(p.is_v ? a.c.v : a.c.k) +
+                   p.row * (D / KV4_GROUP) + p.piece;
+    uint8_t* scales = (p.is_v ? a.c.v_scale : a.c.k_scale) + p.row * (D / KV4_GROUP) + p.piece;
+    Group<T> g[U];
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T); ++i) g.w[i] = __ldcs(src + i);
-    uint32_t sc;
-    const uint2 c = quantise<T>(g, &sc);
-    reinterpret_cast<uint2*>(p.is_v ? a.c.v : a.c.k)[p.row * (D / KV4_GROUP) + p.piece] = c;
-    (p.is_v ? a.c.v_scale : a.c.k_scale)[p.row * (D / KV4_GROUP) + p.piece] = (uint8_t)sc;
+    for (int u = 0; u < U; ++u)
+        if (p.i + u * p.step < p.n) {
+            const uint4* at =
+                reinterpret_cast<const uint4*>(src + (long long)u * p.step * a.row_stride);
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T); ++i) g[u].w[i] = __ldcs(at + i);
+        }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (p.i + u * p.step >= p.n) break;
+        uint32_t sc;
+        codes[(size_t)(u * p.step) * (D / KV4_GROUP)] = quantise<T>(g[u], &sc);
+        scales[(size_t)(u * p.step) * (D / KV4_GROUP)] = (uint8_t)sc;
+    }
 }
 
 template <typename T, int D>
@@ -207,7 +219,7 @@ template <bool STORE>
 cudaError_t launch_rows(const Kv4Rows& s, const void* k_src, const void* v_src, void* k_dst,
                         void* v_dst, const Kv4Ptrs& c, cudaStream_t st) {
     const int pieces = s.head_dim / (STORE ? KV4_GROUP : s.bf16 ? 8 : 4),
-              unroll = STORE ? 1 : LOAD_UNROLL;
+              unroll = !STORE ? LOAD_UNROLL : s.bf16 ? 2 : 1;
     // as many pieces of a head as there are, up to a block; the rest of the block
     // takes further heads
     const long long items = (long long)s.n * pieces;
