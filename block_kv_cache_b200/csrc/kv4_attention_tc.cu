@@ -98,9 +98,10 @@ struct M4 {
     static constexpr int OFF_ML = OFF_V + STAGES * KV;           // float2 per row
     static constexpr int OFF_BAR = OFF_ML + 256 * 8;
     static constexpr int TOTAL = 1024 + OFF_BAR + 512;
-    // after the tiles, the output: [128 MT][D] f32, 16-byte pieces swapped by row
+    // after the tiles, the output: [256][D] f32, 16-byte pieces swapped by row (with
+    // one tile of rows, of either warpgroup's positions), and weights in Q's place
     static constexpr int OFF_O = OFF_K;
-    static_assert(128 * MT * D * 4 <= OFF_ML - OFF_K, "output");
+    static_assert(256 * D * 4 <= OFF_ML - OFF_K && 8 * 256 * 4 <= MT * DC * QC, "output");
     static_assert(TOTAL <= 227 * 1024, "shared memory");
     static constexpr uint32_t TMEM_O = 4 * M4_KT;                // S: [warpgroup][2] of 64
     static constexpr uint32_t TMEM = 512;
@@ -184,10 +185,10 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     auto tile_of = [&](int w, int j) { return MT == 2 ? j : 2 * j + w; };
     bool ok = true;
     // four columns of a finished row, rounded once
-    auto store4 = [&](int row, int c, float4 v, float inv) {
+    auto store4 = [&](bf16* at, float4 v, float inv) {
         const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
         const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(a.out + RowAt(a, h, row0 + row).at(a, bb, D) + 4 * c) =
+        *reinterpret_cast<uint2*>(at) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                        *reinterpret_cast<const uint32_t*>(&hi));
     };
@@ -457,7 +458,7 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         // ---- outputs: a thread has a row, in TMEM; through shared memory (in the
         // tiles' place) to whole rows per warp
         const uint32_t o_at = tmem + lanes + S::TMEM_O + w * D;
-        float4* orow = reinterpret_cast<float4*>(smem + S::OFF_O) + r * (D / 4);
+        float4* orow = reinterpret_cast<float4*>(smem + S::OFF_O) + (w * 128 + lr) * (D / 4);
         float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);
         // a row's last word, by its thread: its maximum and sum for the other splits,
         // or, of the only one, what its output is multiplied with
@@ -466,61 +467,72 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             if (r < own && a.lse) a.lse[RowAt(a, h, row0 + r).lse(a, bb)] = kv4_lse(m, l);
             return make_float2(l == 0.f ? 0.f : 1.f / l, 0.f);   // nothing visible: 0
         };
-        ml[MT == 2 ? r : 128 * w + lr] = MT == 2 ? settle() : make_float2(m, l);
+        if (MT == 1) ml[128 * w + lr] = make_float2(m, l);
         bar_sync(1, 32 * M4_SOFT);           // all tiles have been read
         float f = 1.f;
-        bool add = false;                    // one tile of rows: both warpgroups have them
-        auto give = [&]() {
-#pragma unroll 4
-            for (int c = 0; c < D; c += 16) {
-                float o[16];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = 0.f;
-                if (mine > 0) {
-                    tmem_ld<16>(o_at + c, o);
-                    tmem_wait_ld();
-                }
-#pragma unroll
-                for (int x = 0; x < 16; x += 4) {
-                    float4* to = orow + (((c + x) >> 2) ^ (r & 7));
-                    float4 v = add ? *to : make_float4(0.f, 0.f, 0.f, 0.f);
-                    v.x += o[x] * f;
-                    v.y += o[x + 1] * f;
-                    v.z += o[x + 2] * f;
-                    v.w += o[x + 3] * f;
-                    *to = v;
-                }
-            }
-        };
-        if constexpr (MT == 2) {
-            give();
-            __syncwarp();
-        } else {
-            // (max, sum) of the other warpgroup's half of the positions
+        if constexpr (MT == 1) {
+            // (max, sum) of the other warpgroup's half of the positions: both halves
+            // under the common maximum
             const float2 other = ml[128 * (w ^ 1) + lr];
             const float mn = fmaxf(m, other.x), ms = mn == -INFINITY ? 0.f : mn;
             f = ex2(m - ms);
             l = l * f + other.y * ex2(other.x - ms);
             m = mn;
-            if (w == 1) give();
-            bar_sync(1, 32 * M4_SOFT);
-            if (w == 0) {
-                ml[r] = settle();
-                add = true;
-                give();
-            }
-            bar_sync(1, 32 * M4_SOFT);
         }
+#pragma unroll 4
+        for (int c = 0; c < D; c += 16) {
+            float o[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = 0.f;
+            if (mine > 0) {
+                tmem_ld<16>(o_at + c, o);
+                tmem_wait_ld();
+            }
+#pragma unroll
+            for (int x = 0; x < 16; x += 4)
+                orow[((c + x) >> 2) ^ (lr & 7)] =
+                    make_float4(o[x] * f, o[x + 1] * f, o[x + 2] * f, o[x + 3] * f);
+        }
+        if (MT == 1) bar_sync(1, 32 * M4_SOFT);
+        if (MT == 2 || w == 0) ml[r] = settle();
+        if (MT == 1) bar_sync(1, 32 * M4_SOFT);
+        else __syncwarp();
+        // row k of this warp, columns [4c, 4c + 4) for lane c; both halves' sum
+        constexpr int LR = D / 4, RX = 32 / LR, RW = MT == 2 ? 32 : 16;
+        const int first = MT == 2 ? w * 128 + q * 32 : warp * 16, c = lane % LR;
+        float4* all = reinterpret_cast<float4*>(smem + S::OFF_O);
+        auto fetch = [&](int row) {
+            float4 v = all[row * (D / 4) + (c ^ (row & 7))];
+            if constexpr (MT == 1) {
+                const float4 y = all[(128 + row) * (D / 4) + (c ^ (row & 7))];
+                v.x += y.x;
+                v.y += y.y;
+                v.z += y.z;
+                v.w += y.w;
+            }
+            return v;
+        };
         if (a.cluster == 1) {
-            constexpr int LR = D / 4, RX = 32 / LR;              // lanes of a row, rows at once
-            const int first = MT == 2 ? w * 128 + q * 32 : warp * 16;
+            // lane k knows where the warp's k-th row goes
+            const int row_k = first + lane;
+            const unsigned long long at_k =
+                lane < RW && row_k < own ? reinterpret_cast<unsigned long long>(
+                                               a.out + RowAt(a, h, row0 + row_k).at(a, bb, D))
+                                         : 0;
+            const float inv_k = lane < RW ? ml[row_k].x : 0.f;
 #pragma unroll 8
-            for (int k = 0; k < (MT == 2 ? 32 : 16); k += RX) {
-                const int row = first + k + lane / LR, c = lane % LR;
-                if (row >= own) continue;
-                const float4 v = (reinterpret_cast<const float4*>(smem + S::OFF_O) +
-                                  row * (D / 4))[c ^ (row & 7)];
-                store4(row, c, v, ml[row].x);
+            for (int k = 0; k < RW; k += RX) {
+                const int from = k + lane / LR;
+                const unsigned long long at = __shfl_sync(0xffffffffu, at_k, from);
+                const float inv = __shfl_sync(0xffffffffu, inv_k, from);
+                const float4 v = fetch(first + from);
+                if (at) store4(reinterpret_cast<bf16*>(at) + 4 * c, v, inv);
+            }
+        } else if constexpr (MT == 1) {
+#pragma unroll 8
+            for (int k = 0; k < RW; k += RX) {
+                const int row = first + k + lane / LR;
+                all[row * (D / 4) + (c ^ (row & 7))] = fetch(row);
             }
         }
     }
@@ -532,46 +544,84 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     }
     if (a.cluster > 1) {
         // ---- several splits, joined over the cluster: rank c takes rows c, c +
-        // cluster, ..., a warp per 128 columns
+        // cluster, ... First what each split's part of them is multiplied with, a
+        // thread per row; then the rows, D / 4 lanes each, all loads of UR at once.
         cluster_sync();
-        constexpr int LR = D / 4, RX = 32 / LR;
+        constexpr int LR = D / 4, RX = 32 / LR, UR = 5;
         const int rank = split % a.cluster, c4 = lane % LR;
         const int mine_rows = (own + a.cluster - 1 - rank) / a.cluster;
-#pragma unroll 2
-        for (int k = warp * RX + lane / LR; k < mine_rows; k += M4_THREADS / 32 * RX) {
+        float* wt = reinterpret_cast<float*>(smem + S::OFF_Q);   // [8][256]
+        for (int k = threadIdx.x; k < mine_rows; k += M4_THREADS) {
             const int row = k * a.cluster + rank;
-            const uint32_t o_at = sb + S::OFF_O + (row * (D / 4) + (c4 ^ (row & 7))) * 16;
             float2 p[8];
-            float4 v[8];
+            float M = -INFINITY, sum = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-                if (c < a.cluster) {         // all remote loads first
-                    p[c] = ld_cluster_f2(cluster_map(sb + S::OFF_ML + row * 8, c));
-                    v[c] = ld_cluster_f4(cluster_map(o_at, c));
-                }
-            float M = -INFINITY, sum = 0.f;
+                if (c < a.cluster) p[c] = ld_cluster_f2(cluster_map(sb + S::OFF_ML + row * 8, c));
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 if (c < a.cluster) M = fmaxf(M, p[c].x);
             const float Ms = M == -INFINITY ? 0.f : M;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
                 if (c < a.cluster) {
-                    const float f = ex2(p[c].x - Ms);
-                    sum += p[c].y * f;
-                    acc.x += v[c].x * f;
-                    acc.y += v[c].y * f;
-                    acc.z += v[c].z * f;
-                    acc.w += v[c].w * f;
+                    p[c].x = ex2(p[c].x - Ms);
+                    sum += p[c].y * p[c].x;
                 }
+            float inv = 1.f;
             if (a.parts > 1) {
-                const size_t at = ((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + row;
-                *reinterpret_cast<float4*>(a.part + at * D + 4 * c4) = acc;
-                if (c4 == 0) a.part_ml[at] = make_float2(M, sum);
+                a.part_ml[((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + row] =
+                    make_float2(M, sum);
             } else {
-                store4(row, c4, acc, sum == 0.f ? 0.f : 1.f / sum);
-                if (a.lse && c4 == 0) a.lse[RowAt(a, h, row0 + row).lse(a, bb)] = kv4_lse(M, sum);
+                inv = sum == 0.f ? 0.f : 1.f / sum;              // nothing visible: 0
+                if (a.lse) a.lse[RowAt(a, h, row0 + row).lse(a, bb)] = kv4_lse(M, sum);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                if (c < a.cluster) wt[c * 256 + k] = p[c].x * inv;
+        }
+        __syncthreads();
+        constexpr int KX = M4_THREADS / 32 * RX;                 // rows of the block at once
+        for (int k0 = warp * RX + lane / LR; k0 < mine_rows; k0 += UR * KX) {
+            float4 acc[UR];
+#pragma unroll
+            for (int x = 0; x < UR; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = 0; c < a.cluster; c += 2) {
+                float4 v[2][UR];
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < UR; ++x) {
+                        const int k = k0 + x * KX, row = k * a.cluster + rank;
+                        if (c + y < a.cluster && k < mine_rows)
+                            v[y][x] = ld_cluster_f4(cluster_map(
+                                sb + S::OFF_O + (row * (D / 4) + (c4 ^ (row & 7))) * 16, c + y));
+                    }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < UR; ++x) {
+                        const int k = k0 + x * KX;
+                        if (c + y < a.cluster && k < mine_rows) {
+                            const float f = wt[(c + y) * 256 + k];
+                            acc[x].x += v[y][x].x * f;
+                            acc[x].y += v[y][x].y * f;
+                            acc[x].z += v[y][x].z * f;
+                            acc[x].w += v[y][x].w * f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int x = 0; x < UR; ++x) {
+                const int k = k0 + x * KX, row = k * a.cluster + rank;
+                if (k >= mine_rows) continue;
+                if (a.parts > 1) {
+                    const size_t at =
+                        ((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + row;
+                    *reinterpret_cast<float4*>(a.part + at * D + 4 * c4) = acc[x];
+                } else {
+                    store4(a.out + RowAt(a, h, row0 + row).at(a, bb, D) + 4 * c4, acc[x], 1.f);
+                }
             }
         }
         cluster_sync();                      // no block leaves while others read its memory
