@@ -23,7 +23,7 @@ struct GenGraph {
     uint64_t model = 0;                           // fdl_model id
     const void* ws = nullptr;
     size_t ws_bytes = 0;
-    int b = 0, P = 0, gen = 0, B = 0, mode = 0;
+    int b = 0, P = 0, gen = 0, B = 0, mode = 0, kv = 0;
     float tau = 0.f;
     const void* bias_tok = nullptr;
     const void* bias_val = nullptr;
@@ -916,12 +916,15 @@ __global__ void gather_bias_kernel(const int32_t* __restrict__ btok,
 struct GenLayout {
     size_t kc, vc, h_full, x_full, q_full, o_full, f_full, h_blk, x_blk, q_blk, o_blk, f_blk,
         xn, conf, tok, masked, counts, maps, tail_map, tail_blk, bias_tok, bias_val, rope, lm_ws,
-        x, steps, seq_map, row_map_c, bias_tok_c, bias_val_c, ps_maps, total;
-    size_t kv_layer;    // bytes of one layer's K (or V) cache
+        x, steps, seq_map, row_map_c, bias_tok_c, bias_val_c, ps_maps, kv4, kv4_ws, total;
+    size_t kv_layer;    // bytes of one layer's K (or V) cache, bf16
+    size_t kv4_codes, kv4_scales;   // ... of its codes and of its scales, 4-bit cache
+    size_t kv4_ws_bytes;
     size_t lm_bytes;
 };
 
-GenLayout gen_layout(const fdl_model_desc& d, int b, int L, int B, size_t lm_bytes) {
+GenLayout gen_layout(const fdl_model_desc& d, int b, int L, int B, size_t lm_bytes, int kv,
+                     size_t kv4_ws_bytes) {
     GenLayout g{};
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -933,8 +936,18 @@ GenLayout gen_layout(const fdl_model_desc& d, int b, int L, int B, size_t lm_byt
     const size_t rf = (size_t)b * L, rb = (size_t)b * B;
     const int nblk = (L + B - 1) / B;
     g.kv_layer = (size_t)b * Hkv * L * hd * 2;
-    g.kc = take(g.kv_layer * d.n_layers);
-    g.vc = take(g.kv_layer * d.n_layers);
+    // bf16: every layer's cache; 4-bit: one layer's fresh rows beside the codes and
+    // scales of all
+    const int bf16_layers = kv == FDL_KV_4BIT ? 1 : d.n_layers;
+    g.kc = take(g.kv_layer * bf16_layers);
+    g.vc = take(g.kv_layer * bf16_layers);
+    if (kv == FDL_KV_4BIT) {
+        g.kv4_codes = ((size_t)b * Hkv * L * (hd / 2) + 255) & ~(size_t)255;
+        g.kv4_scales = ((size_t)b * Hkv * L * (hd / 16) + 255) & ~(size_t)255;
+        g.kv4 = take(2 * (g.kv4_codes + g.kv4_scales) * d.n_layers);
+        g.kv4_ws_bytes = kv4_ws_bytes;
+        g.kv4_ws = take(kv4_ws_bytes);
+    }
     g.h_full = take(rf * D * 4);
     g.x_full = take(rf * D * 2);
     g.q_full = take(rf * Hq * hd * 2);
@@ -978,12 +991,55 @@ GenLayout gen_layout(const fdl_model_desc& d, int b, int L, int B, size_t lm_byt
 struct GenRun {
     fdl_ctx* ctx;
     const fdl_model* m;
-    int b, P, gen, B, L, mode;
+    int b, P, gen, B, L, mode, kv;
     float tau;
     const int32_t* bias_tok;
     const float* bias_val;
     GenLayout g;
     char* base;
+
+    // layer li's 4-bit cache, and its rows as they lie in the bf16 scratch
+    fdl_kv4_cache kv4_cache(int li) const {
+        char* p = base + g.kv4 + 2 * (g.kv4_codes + g.kv4_scales) * li;
+        return fdl_kv4_cache{p, p + 2 * g.kv4_codes, p + g.kv4_codes,
+                             p + 2 * g.kv4_codes + g.kv4_scales};
+    }
+    fdl_kv4_rows_desc kv4_scratch_rows() const {
+        const int Hkv = m->d.n_kv_heads;
+        return fdl_kv4_rows_desc{b, Hkv, 128, L, FDL_BF16, (int64_t)Hkv * L * 128, 128,
+                                 (int64_t)L * 128};
+    }
+    // The attention half of layer li with its K/V in 4 bits, rows at [pos0, pos0 + n) of
+    // every sequence. full: attention over the fresh rows, and, for those before
+    // pos0, the cache's; the refresh (pos0 = 0) stores them. Otherwise the block's rows
+    // are stored and attend over the cache.
+    int kv4_layer(int li, const fdl_qkv_desc& qd, float* h, void* xb, void* q, void* o, bool full,
+                  cudaStream_t st) const {
+        const fdl_model_desc& d = m->d;
+        const fdl_layer_weights& W = m->layers[li];
+        const int Hq = d.n_q_heads, Hkv = d.n_kv_heads, pos0 = qd.pos0, n = qd.rows_per_seq;
+        void* stream = (void*)st;
+        char *kl = base + g.kc, *vl = base + g.vc;
+        const size_t at0 = (size_t)pos0 * 128 * 2;   // row pos0 of a head in the scratch
+        const fdl_kv4_cache c = kv4_cache(li);
+        const fdl_kv4_rows_desc rd = kv4_scratch_rows();
+        int rc = fdl_rmsnorm(ctx, qd.rows, d.hidden, h, nullptr, W.attn_norm, d.rms_eps, xb,
+                             stream);
+        if (!rc) rc = fdl_qkv_rope_store(ctx, &qd, xb, W.w_qkv, W.bias, (const float*)at(g.rope),
+                                         q, kl, vl, stream);
+        if (rc) return rc;
+        if (!full) {
+            rc = fdl_kv4_store(ctx, &rd, kl + at0, vl + at0, pos0, n, &c, stream);
+            const fdl_kv4_attn_desc ad{b, Hq, Hkv, 128, L, pos0, n, FDL_BF16, 0.f, -1, -1, 0};
+            return rc ? rc : fdl_kv4_attention(ctx, &ad, q, &c, nullptr, o, nullptr,
+                                               at(g.kv4_ws), g.kv4_ws_bytes, stream);
+        }
+        if (pos0 > 0) rc = fdl_kv4_load(ctx, &rd, &c, 0, pos0, kl, vl, stream);
+        const fdl_attn_desc ad{b, Hq, Hkv, 128, L, pos0, n, FDL_BF16, 0.f};
+        if (!rc) rc = fdl_full_attention(ctx, &ad, q, kl, vl, o, stream);
+        if (!rc && pos0 == 0) rc = fdl_kv4_store(ctx, &rd, kl, vl, 0, L, &c, stream);
+        return rc;
+    }
 
     void* at(size_t off) const { return static_cast<void*>(base + off); }
     int32_t* x() const { return (int32_t*)at(g.x); }
@@ -1033,7 +1089,9 @@ struct GenRun {
             void* kl = base + g.kc + g.kv_layer * li;
             void* vl = base + g.vc + g.kv_layer * li;
             const fdl_qkv_desc qd{rows, D, Hq, Hkv, hd, nb > 0 ? nb : b, L, n, pos0, L};
-            if (full) {
+            if (kv == FDL_KV_4BIT) {
+                rc = kv4_layer(li, qd, h, xb, q, o, full, st);
+            } else if (full) {
                 rc = fdl_rmsnorm(ctx, rows, D, h, nullptr, W.attn_norm, d.rms_eps, xb, stream);
                 if (!rc) rc = qkv_rope_store_mapped(ctx, &qd, xb, W.w_qkv, W.bias, rope, q, kl,
                                                     vl, stream, seq_map, b);
@@ -1222,6 +1280,7 @@ __global__ void loop_cond_kernel(cudaGraphConditionalHandle h, const int32_t* __
 bool same_key(const GenGraph* c, const GenRun& r, size_t ws_bytes) {
     return c && c->exec && c->model == r.m->id && c->ws == r.base && c->ws_bytes == ws_bytes &&
            c->b == r.b && c->P == r.P && c->gen == r.gen && c->B == r.B && c->mode == r.mode &&
+           c->kv == r.kv &&
            c->tau == r.tau && c->bias_tok == r.bias_tok && c->bias_val == r.bias_val;
 }
 
@@ -1314,6 +1373,7 @@ int run_device_loop(const GenRun& r, cudaStream_t st) {
         c->gen = r.gen;
         c->B = r.B;
         c->mode = r.mode;
+        c->kv = r.kv;
         c->tau = r.tau;
         c->bias_tok = r.bias_tok;
         c->bias_val = r.bias_val;
@@ -1333,6 +1393,14 @@ bool model_desc_ok(const fdl_model_desc* d) {
 size_t lm_ws_bytes(fdl_ctx* ctx, const fdl_model_desc& d, int rows) {
     const fdl_lmhead_desc ld{rows, d.hidden, d.vocab, FDL_BF16};
     const size_t n = fdl_lmhead_workspace_bytes(ctx, &ld);
+    return n > 16 ? n : 16;
+}
+
+// Scratch of a decode's 4-bit attention (the same for every block start).
+size_t kv4_ws_bytes(fdl_ctx* ctx, const fdl_model_desc& d, int b, int L, int B, int kv) {
+    if (kv != FDL_KV_4BIT || B > L) return 16;
+    const fdl_kv4_attn_desc ad{b, d.n_q_heads, d.n_kv_heads, 128, L, 0, B, FDL_BF16, 0.f, -1, -1, 0};
+    const size_t n = fdl_kv4_attention_workspace_bytes(ctx, &ad);
     return n > 16 ? n : 16;
 }
 
@@ -1380,8 +1448,15 @@ int fdl_model_destroy(fdl_model* model) {
 
 size_t fdl_generate_workspace_bytes(fdl_ctx* ctx, const fdl_model* m, int batch, int seq_len,
                                     int block) {
+    return fdl_generate_workspace_bytes_kv(ctx, m, batch, seq_len, block, FDL_KV_BF16);
+}
+
+size_t fdl_generate_workspace_bytes_kv(fdl_ctx* ctx, const fdl_model* m, int batch, int seq_len,
+                                       int block, int kv) {
     if (!ctx || !m || batch < 1 || seq_len < 1 || block < 1 || block > 128) return 0;
-    return gen_layout(m->d, batch, seq_len, block, lm_ws_bytes(ctx, m->d, batch * block)).total;
+    if (kv != FDL_KV_BF16 && kv != FDL_KV_4BIT) return 0;
+    return gen_layout(m->d, batch, seq_len, block, lm_ws_bytes(ctx, m->d, batch * block), kv,
+                      kv4_ws_bytes(ctx, m->d, batch, seq_len, block, kv)).total;
 }
 
 int fdl_generate(fdl_ctx* ctx, const fdl_model* m, const int32_t* prompt, int b, int P, int gen,
@@ -1402,6 +1477,7 @@ int fdl_generate(fdl_ctx* ctx, const fdl_model* m, const int32_t* prompt, int b,
     r.B = B;
     r.tau = tau;
     r.mode = opts ? opts->cache : FDL_CACHE_DUAL;
+    r.kv = opts ? opts->kv : FDL_KV_BF16;
     const bool device_loop = opts && opts->device_loop;
     const int batching = opts ? opts->batching : FDL_BATCH_LOCKSTEP;
     const bool compact = batching == FDL_BATCH_COMPACT;
@@ -1410,6 +1486,11 @@ int fdl_generate(fdl_ctx* ctx, const fdl_model* m, const int32_t* prompt, int b,
         return fail(FDL_EINVAL, "generate: unknown batching %d", batching);
     if (r.mode != FDL_CACHE_DUAL && r.mode != FDL_CACHE_PREFIX && r.mode != FDL_CACHE_NONE)
         return fail(FDL_EINVAL, "generate: unknown cache mode %d", r.mode);
+    if (r.kv != FDL_KV_BF16 && r.kv != FDL_KV_4BIT)
+        return fail(FDL_EINVAL, "generate: unknown K/V format %d", r.kv);
+    if (r.kv == FDL_KV_4BIT && (r.mode == FDL_CACHE_NONE || batching != FDL_BATCH_LOCKSTEP))
+        return fail(FDL_EINVAL, "generate: a 4-bit cache needs the DualCache or PrefixCache mode "
+                    "and lockstep batching");
     r.bias_tok = opts ? opts->bias_tok : nullptr;
     r.bias_val = opts ? opts->bias_val : nullptr;
     if ((r.bias_tok == nullptr) != (r.bias_val == nullptr))
@@ -1425,7 +1506,8 @@ int fdl_generate(fdl_ctx* ctx, const fdl_model* m, const int32_t* prompt, int b,
         return fail(FDL_EINVAL, "generate: the PrefixCache mode needs the block starts at "
                     "multiples of 32 (prompt_len and block)");
     const int rf = b * r.L, rb = b * B;
-    r.g = gen_layout(d, b, r.L, B, lm_ws_bytes(ctx, d, rb));
+    r.g = gen_layout(d, b, r.L, B, lm_ws_bytes(ctx, d, rb), r.kv,
+                     kv4_ws_bytes(ctx, d, b, r.L, B, r.kv));
     if (!ws || ws_bytes < r.g.total)
         return fail(FDL_EWORKSPACE, "generate: workspace of %zu bytes needed", r.g.total);
     if (((uintptr_t)ws & 255u) != 0) return fail(FDL_EINVAL, "generate: ws must be 256-byte aligned");

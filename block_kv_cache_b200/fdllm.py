@@ -36,7 +36,7 @@ EXPORTS = ("fdl_abi_version", "fdl_create", "fdl_destroy", "fdl_last_error",
            "fdl_full_attention", "fdl_ffn", "fdl_qkv_attention", "fdl_model_create",
            "fdl_model_destroy", "fdl_generate_workspace_bytes", "fdl_generate",
            "fdl_kv4_store", "fdl_kv4_load", "fdl_kv4_attention_workspace_bytes",
-           "fdl_kv4_attention")
+           "fdl_kv4_attention", "fdl_generate_workspace_bytes_kv")
 
 
 class AttnDesc(ctypes.Structure):
@@ -117,9 +117,10 @@ CACHE_MODES = {"dual": FDL_CACHE_DUAL, "prefix": FDL_CACHE_PREFIX, "none": FDL_C
 class GenerateOpts(ctypes.Structure):
     _fields_ = [("cache", ctypes.c_int), ("device_loop", ctypes.c_int),
                 ("bias_tok", ctypes.c_void_p), ("bias_val", ctypes.c_void_p),
-                ("batching", ctypes.c_int)]
+                ("batching", ctypes.c_int), ("kv", ctypes.c_int)]
 
 
+KV_FORMATS = {"bf16": 0, "4bit": 1}
 BATCHING = {"lockstep": 0, "compact": 1, "per_sequence": 2}
 
 
@@ -182,6 +183,8 @@ def load() -> ctypes.CDLL:
     L.fdl_model_destroy.argtypes = [vp]
     L.fdl_generate_workspace_bytes.argtypes = [vp, vp, i, i, i]
     L.fdl_generate_workspace_bytes.restype = sz
+    L.fdl_generate_workspace_bytes_kv.argtypes = [vp, vp, i, i, i, i]
+    L.fdl_generate_workspace_bytes_kv.restype = sz
     L.fdl_generate.argtypes = [vp, vp, vp, i, i, i, i, fl, ctypes.POINTER(GenerateOpts), vp,
                                ctypes.POINTER(i), vp, sz, vp]
     L.fdl_kv4_store.argtypes = [vp, ctypes.POINTER(Kv4RowsDesc), vp, vp, i, i,
@@ -669,7 +672,7 @@ class Context:
 
     def generate(self, model: Model, prompt, gen_len, *, block=32, tau=0.9, cache="dual",
                  bias_tok=None, bias_val=None, device_loop=False, batching="lockstep",
-                 stream=None):
+                 kv="bf16", stream=None):
         """The whole decode in the library (fdl_generate). prompt [b, P] int32,
         a CUDA tensor or a host tensor (then copied to the device first, and
         the result copied back to a host tensor: the public call with host
@@ -681,7 +684,8 @@ class Context:
         it does). batching (DualCache, host loop for the last two): "lockstep",
         "compact" (cached steps only on the sequences with masked positions
         left in the block) or "per_sequence" (each sequence moves to its next
-        block on its own). Returns (x [b, P + gen_len] int32, steps)."""
+        block on its own). kv: how the layers' K/V are held, "bf16" or "4bit"
+        (DualCache or PrefixCache, lockstep). Returns (x [b, P + gen_len] int32, steps)."""
         on_host = not prompt.is_cuda
         dev = torch.device("cuda", self.device)
         if on_host:
@@ -692,7 +696,8 @@ class Context:
             _need(bias_tok, "bias_tok", torch.int32, 2)
             _need(bias_val, "bias_val", torch.float32, 2)
         L = load()
-        n = L.fdl_generate_workspace_bytes(self._h, model._h, b, P + gen_len, int(block))
+        n = L.fdl_generate_workspace_bytes_kv(self._h, model._h, b, P + gen_len, int(block),
+                                              KV_FORMATS[kv])
         if n == 0:
             raise ValueError("generate: bad shape")
         if getattr(self, "_gen_ws", None) is None or self._gen_ws.numel() < n:
@@ -704,7 +709,7 @@ class Context:
         opts = GenerateOpts(CACHE_MODES[cache], int(bool(device_loop)),
                             None if bias_tok is None else bias_tok.data_ptr(),
                             None if bias_val is None else bias_val.data_ptr(),
-                            BATCHING[batching])
+                            BATCHING[batching], KV_FORMATS[kv])
         _check(L.fdl_generate(self._h, model._h, _ptr(prompt), b, P, int(gen_len), int(block),
                               float(tau), ctypes.byref(opts), _ptr(x), ctypes.byref(steps),
                               _ptr(ws), ws.numel(), _stream(stream)))

@@ -540,6 +540,23 @@ FDL_API int fdl_model_destroy(fdl_model* model);
 FDL_API size_t fdl_generate_workspace_bytes(fdl_ctx* ctx, const fdl_model* model, int batch,
                                             int seq_len, int block);
 
+/* The same for a cache held in `kv` (fdl_kv_format); fdl_generate_workspace_bytes
+ * is that of FDL_KV_BF16. In FDL_KV_4BIT every layer's cache takes 4.5 bits per
+ * value, beside one layer's K/V in bf16. */
+FDL_API size_t fdl_generate_workspace_bytes_kv(fdl_ctx* ctx, const fdl_model* model, int batch,
+                                               int seq_len, int block, int kv);
+
+/* How fdl_generate holds the layers' K/V between steps. */
+typedef enum {
+    FDL_KV_BF16 = 0,
+    FDL_KV_4BIT = 1   /* quantised as they are written (fdl_kv4_store): a refresh attends
+                         over its own fresh K/V and then stores them; a DualCache step
+                         stores the block's rows and attends over the 4-bit cache
+                         (fdl_kv4_attention); a PrefixCache step reads the prefix back
+                         (fdl_kv4_load) and attends over it and its own fresh K/V.
+                         FDL_CACHE_DUAL or FDL_CACHE_PREFIX, FDL_BATCH_LOCKSTEP. */
+} fdl_kv_format;
+
 /* Which K/V a decode step after a block's first reuses (Fast-dLLM README,
  * usage flags and the evaluation table's "+cache" columns; aibase news
  * "Innovations" 1). A block's first step is always the full forward that
@@ -578,7 +595,7 @@ typedef struct {
      * the block (the condition is set by a small kernel after each step); the
      * host synchronises once per decode. The executable graph is kept in the
      * context and launched again by the next call with the same model,
-     * workspace, shapes, tau, cache mode and bias pointers; the first call
+     * workspace, shapes, tau, cache mode, K/V format and bias pointers; the first call
      * captures and instantiates it. */
     int device_loop;
     /* Optional planted logit bias per generated position (a synthetic workload
@@ -589,6 +606,7 @@ typedef struct {
     const int32_t* bias_tok;  /* [batch, gen_len] int32 device, entries in [0, V), or NULL */
     const float* bias_val;    /* [batch, gen_len] f32 device; required iff bias_tok */
     int batching;             /* fdl_batching */
+    int kv;                   /* fdl_kv_format */
 } fdl_generate_opts;
 
 /* Decode gen_len positions after the prompts of `batch` sequences.
@@ -600,10 +618,10 @@ typedef struct {
  *           and block too, so that every block starts at a multiple of 32)
  *   tau     threshold in [0, 1] (tau = 1 decodes exactly one position per step)
  *   opts    cache mode, loop, optional planted bias, batching; NULL =
- *           FDL_CACHE_DUAL, host loop, no bias, FDL_BATCH_LOCKSTEP
+ *           FDL_CACHE_DUAL, host loop, no bias, FDL_BATCH_LOCKSTEP, FDL_KV_BF16
  *   *steps_out (host) the decode steps taken (refresh steps included)
- *   ws      device workspace of fdl_generate_workspace_bytes bytes, 256-byte
- *           aligned
+ *   ws      device workspace of fdl_generate_workspace_bytes bytes (with opts->kv,
+ *           fdl_generate_workspace_bytes_kv), 256-byte aligned
  * With the host loop every step reads `batch` 4-byte counters back to decide
  * between the next cached step and the next block; with opts->device_loop the
  * steps are sequenced on the device. The call returns when the decode is
