@@ -253,25 +253,34 @@ class Kv4Cache:
     def __init__(self, k, k_scale, v, v_scale):
         try:
             b, h, L, half = shape = k.shape
-            if half not in (32, 64):
-                raise ValueError
+            scales, dev, u8 = (b, h, L, half // 8), k.get_device(), torch.uint8
+            right = ((half == 64 or half == 32) and dev >= 0
+                     and v.shape == shape and k_scale.shape == scales and v_scale.shape == scales
+                     and k.dtype is u8 and k_scale.dtype is u8 and v.dtype is u8
+                     and v_scale.dtype is u8 and k_scale.get_device() == dev
+                     and v.get_device() == dev and v_scale.get_device() == dev
+                     and k.is_contiguous() and k_scale.is_contiguous() and v.is_contiguous()
+                     and v_scale.is_contiguous())
         except (AttributeError, ValueError):
-            raise ValueError("Kv4Cache: k must be [b, Hkv, L, 32 or 64] code bytes (head_dim 64 "
-                             "or 128)") from None
-        scales, device = (b, h, L, half // 8), k.get_device()
-        for t, n, want in ((k, "k", shape), (k_scale, "k_scale", scales), (v, "v", shape),
-                           (v_scale, "v_scale", scales)):
-            if t.dtype is not torch.uint8 or device < 0 or t.get_device() != device \
-                    or not t.is_contiguous():
-                raise TypeError(f"Kv4Cache: {n} must be a contiguous uint8 CUDA tensor on k's "
-                                "device")
-            if t.shape != want:
-                raise ValueError(f"Kv4Cache: {n} has shape {tuple(t.shape)}, not {tuple(want)}")
+            right = False
+        if not right:
+            self._refuse(k, k_scale, v, v_scale)
         self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
         self.batch, self.n_kv_heads, self.seq_len, self.head_dim = b, h, L, 2 * half
-        self.device_index = device
+        self.device_index = dev
         self.buffers = Kv4Buffers(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),
                                   v_scale.data_ptr())
+
+    @staticmethod
+    def _refuse(k, k_scale, v, v_scale):
+        for t, n in ((k, "k"), (k_scale, "k_scale"), (v, "v"), (v_scale, "v_scale")):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.uint8 \
+                    or not t.is_contiguous() or t.get_device() != k.get_device():
+                raise TypeError(f"Kv4Cache: {n} must be a contiguous uint8 CUDA tensor on k's "
+                                "device")
+        raise ValueError("Kv4Cache: k and v must be [b, Hkv, L, d/2], the scales [b, Hkv, L, "
+                         f"d/16], d 64 or 128; not {tuple(k.shape)}, {tuple(k_scale.shape)}, "
+                         f"{tuple(v.shape)}, {tuple(v_scale.shape)}")
 
     @classmethod
     def empty(cls, batch, n_kv_heads, seq_len, head_dim=128, device="cuda"):
