@@ -699,6 +699,8 @@ int kv4_rows(const char* who, const fdl_ctx* ctx, const fdl_kv4_rows_desc* d, in
     if (n < 1 || start < 0 || (int64_t)start + n > d->seq_len)
         return fail(FDL_EINVAL, "%s: rows [%d, %lld) outside [0, %d)", who, start,
                     (long long)start + n, d->seq_len);
+    if (d->seq_len > FDL_KV4_MAX_SEQ)
+        return fail(FDL_EUNSUPPORTED, "%s: seq_len %d above %d", who, d->seq_len, FDL_KV4_MAX_SEQ);
     if (d->n_kv_heads > 32767)   // two grid rows per head
         return fail(FDL_EUNSUPPORTED, "%s: %d heads are too many for one call", who,
                     d->n_kv_heads);
@@ -731,6 +733,9 @@ int check_kv4_attn(const fdl_kv4_attn_desc* d, fdl::Kv4Attn* out) {
     if (rc) return rc;
     if (d->dtype != FDL_BF16)
         return fail(FDL_EUNSUPPORTED, "kv4_attention: q and out must be bf16");
+    if (d->seq_len > FDL_KV4_MAX_SEQ)
+        return fail(FDL_EUNSUPPORTED, "kv4_attention: seq_len %d above %d", d->seq_len,
+                    FDL_KV4_MAX_SEQ);
     if (d->sinks < 0) return fail(FDL_EINVAL, "kv4_attention: sinks must be >= 0");
     if ((int64_t)d->batch * d->n_q_heads * d->block_len >= ((int64_t)1 << 28))
         return fail(FDL_EUNSUPPORTED, "kv4_attention: too many query rows for one call");

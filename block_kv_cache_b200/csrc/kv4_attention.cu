@@ -6,14 +6,19 @@
 // (Seen::pos maps an index to its position), so a window costs what it shows
 // and no score is masked but those behind the end of a step.
 //
-// Everything between the cache and the output stays in registers. A warp takes
-// steps of 32 visible positions and keeps a running maximum, sum and output of
-// its own for the packed query rows (query i, head j of the kv head's group ->
-// row i * G + j). The codes arrive by cp.async in the warp's own ring in shared
-// memory (positions behind the end arrive as zeros: code 0 under scale 0), and
-// each thread converts exactly the codes that its fragments of the matrix
-// instructions need, so a cached value is converted once per 32 query rows and
-// never written back to memory:
+// Few query rows per kv head (a token's, a short block's): what it costs is reading
+// and converting the cache, (16 + 2) / 16 bytes per 16 values of K and V, so all of
+// it stays in registers between the two. A warp takes steps of 32 visible positions
+// (16 with more than 16 rows) and keeps a running maximum, sum and output of its own
+// for the packed query rows (query i, head j of the kv head's group -> row i * G + j).
+// The codes arrive by cp.async in the warp's own ring in shared memory (positions
+// behind the end arrive as zeros: code 0 under scale 0), and each thread converts
+// exactly the codes that its fragments of the matrix instructions need, so a cached
+// value is converted once per 32 query rows and never written back to memory. That
+// is what mma.sync gives here and tcgen05 does not: its operands have to be stored
+// to shared memory as f16, four times the bytes of the codes, and one of its tiles
+// has 128 rows, of which 4 to 32 would be used (measured with positions as the rows
+// instead: a token over 131072 positions 85 us, a 32 x 7 block over 768 10.9 us).
 //   S = Q K^T   contraction over head_dim; the order of the dimensions is free
 //               as long as Q has the same, so thread t of a quad owns dims
 //               [D/4 t, D/4 (t+1)): one 16-byte load of a key's codes
@@ -25,6 +30,19 @@
 // into the operand of the second; the position that column n of an 8-column
 // tile stands for is chosen so that both products' loads are free of bank
 // conflicts (row_of).
+//
+// The warps of a block join in shared memory, and the blocks of a cluster (the splits
+// of one unit) by st.async into the block that finishes a row, which counts the bytes
+// on a barrier. With more than 8 splits the clusters leave partial results in the
+// workspace and a second kernel joins them.
+//
+// What bounds it (heads of 128; 6.55 TB/s measured copy): one
+// token of 28 heads over 131072 positions of 4, 75.5 MB: 25.2 us with the join, in the
+// steps 5.3 TB/s with the schedulers issuing in 79 % of the cycles (conversion 2
+// cycles per 2 values and multiplication by the scale as many), 2.9 us before the
+// first step and 2.4 for the join. A 32-query block over 768 positions: 7.7 us, of
+// them 1.5 for Q, 2 for the merge. Two blocks of 8 warps per SM with up to 16 rows
+// (one: 29 us); with 32 rows the outputs take the registers of one.
 //
 // Numbers: cached values are exact in f16 (kv4.cuh). Queries are brought to f16
 // by a power of two per row that puts the row's largest value into
@@ -42,12 +60,6 @@ namespace {
 
 constexpr int A4_WARPS = 8, A4_THREADS = A4_WARPS * 32;
 constexpr int A4_CLUSTER = 8;                // splits that join on chip
-#ifndef KS1
-#define KS1 32
-#define KS2 16
-#define OCC1 2
-#define FORCE1 0
-#endif
 
 // c += A (16 x 16, rows) * B (16 x 8, columns), f16 with f32 sums.
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t* a, uint32_t b0,
@@ -76,8 +88,8 @@ __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&r)[1]) {
 
 template <int D, int MT>
 struct A4 {
-    static constexpr int KS = MT == 1 ? KS1 : KS2;               // positions per step of a warp
-    static constexpr int OCC = MT == 1 ? OCC1 : 1;               // blocks per SM
+    static constexpr int KS = MT == 1 ? 32 : 16;                 // positions per step of a warp
+    static constexpr int OCC = MT == 1 ? 2 : 1;                  // blocks per SM
     static constexpr int STAGES = OCC == 2 ? 64 / KS : 96 / KS;  // of a warp's ring
     static constexpr int CB = D / 2, SB = D / KV4_GROUP;         // bytes of a row
     static constexpr int KK = D / 16;                            // k-steps of S

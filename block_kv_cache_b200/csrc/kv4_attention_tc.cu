@@ -19,6 +19,16 @@
 //       positions, and join their outputs at the end.
 // A warp's scores of the next tile are computed while it works on this one.
 //
+// What bounds it: 32 sequences, 32 queries of 28 heads on 4 kv heads of 128, 1024
+// positions: 28.2 us (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the
+// bytes). A block's 8 tiles per split take 1.1 us each: the exponentials, maxima and
+// conversions of two softmax warps per scheduler (1450 cycles when nothing else
+// issues, measured alone) beside the conversion warps. The rest is 4.7 us before the
+// first scores (start, Q) and 3.8 after the last (join, output). Searching the next
+// tile's maximum beside this one's exponentials took 29.5 us, one matrix warp for
+// both warpgroups 37.9. 8 sequences of 32 queries of 32 heads on 8 over a window of
+// 1060 positions: 18.2 us, of which the loop is a third.
+//
 // Numbers as in kv4_attention.cu: f16 operands (cached values exact, queries by a
 // power of two per row), f32 scores, sums and outputs, f16 probabilities at 2^7 to
 // 2^15 at the running maximum, which is raised when it grows by more than 2^8.

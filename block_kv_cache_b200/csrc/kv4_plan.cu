@@ -103,14 +103,14 @@ int most_seen(const Kv4Attn& s) {
     return s.sinks + s.win_hi - s.win_lo;
 }
 
-
 Kv4Plan plan_of(const Kv4Attn& s, int sm_count) {
     Kv4Plan p;
     const int rows = s.block_len * (s.n_q_heads / s.n_kv_heads), seen = most_seen(s);
-    // The tcgen05 kernel takes 12 to 17 us before it is any faster: it is used where
-    // the 32-row blocks of the other would not all run at once (64 units of 128 rows
-    // over 1024 positions: 19 and 29 us) or have much to do (8 units of 192 rows over
-    // 4096: 23 and 26 us; over 1024: 14 and 12 us).
+    // The tcgen05 kernel takes 10 to 15 us before it is any faster: it is used where
+    // the 32-row blocks of the other would not all run at once (tcgen05 and the other,
+    // 64 units of 128 rows over 1024 positions: 18.0 and 29.4 us) or have much to do
+    // (32 units of 64 rows over 4096: 24.5 and 25.8; 8 units of 256 rows over 1024:
+    // 18.1 and 11.9, over 4096, just above the rule's edge: 27.8 and 25.6).
     const long long blocks = (long long)s.batch * s.n_kv_heads * ((rows + 31) / 32);
     p.many = rows > 32 && (blocks > sm_count || blocks * seen > 1100ll * sm_count);
     if (p.many) {

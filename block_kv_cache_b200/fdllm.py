@@ -48,6 +48,7 @@ class AttnDesc(ctypes.Structure):
 
 
 ABI_VERSION = 7
+KV4_MAX_SEQ = 1 << 30
 
 
 class Kv4Buffers(ctypes.Structure):
@@ -244,6 +245,14 @@ def rope_table(theta: float, max_pos: int, head_dim: int):
     return out
 
 
+def _i32(x, name):
+    """An int argument of a call; ctypes would drop the bits above 32."""
+    x = int(x)
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} {x} does not fit in 32 bits")
+    return x
+
+
 class Kv4Cache:
     """One layer's K/V cache in microscaled 4-bit floating point (fdl_kv4_cache): codes k, v
     [b, Hkv, L, d/2] and scales k_scale, v_scale [b, Hkv, L, d/16], uint8 CUDA tensors that the
@@ -254,7 +263,8 @@ class Kv4Cache:
         try:
             b, h, L, half = shape = k.shape
             scales, dev, u8 = (b, h, L, half // 8), k.get_device(), torch.uint8
-            right = ((half == 64 or half == 32) and dev >= 0
+            right = ((half == 64 or half == 32) and dev >= 0 and L <= KV4_MAX_SEQ
+                     and b <= KV4_MAX_SEQ and h <= KV4_MAX_SEQ
                      and v.shape == shape and k_scale.shape == scales and v_scale.shape == scales
                      and k.dtype is u8 and k_scale.dtype is u8 and v.dtype is u8
                      and v_scale.dtype is u8 and k_scale.get_device() == dev
@@ -279,7 +289,7 @@ class Kv4Cache:
                 raise TypeError(f"Kv4Cache: {n} must be a contiguous uint8 CUDA tensor on k's "
                                 "device")
         raise ValueError("Kv4Cache: k and v must be [b, Hkv, L, d/2], the scales [b, Hkv, L, "
-                         f"d/16], d 64 or 128; not {tuple(k.shape)}, {tuple(k_scale.shape)}, "
+                         f"d/16], d 64 or 128, no dimension above 2^30; not {tuple(k.shape)}, {tuple(k_scale.shape)}, "
                          f"{tuple(v.shape)}, {tuple(v_scale.shape)}")
 
     @classmethod
@@ -398,7 +408,7 @@ class Context:
         _need(k_cache, "k_cache", None, 4)
         _need(v_cache, "v_cache", k_cache.dtype, 4)
         b, Hkv, L, d = k_cache.shape
-        n = k_new.shape[1]
+        n = _i32(k_new.shape[1], "n")
         desc = AttnDesc(b, Hkv, Hkv, d, L, 0, 1, _dtype_code(k_cache), 0.0)
         _check(load().fdl_kv_store(self._h, ctypes.byref(desc), _ptr(k_new), _ptr(v_new),
                                    int(start), int(n), _ptr(k_cache), _ptr(v_cache),
@@ -471,10 +481,10 @@ class Context:
         self._kv4_cache(cache)
         if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4 or v_new is None:
             raise ValueError("kv4_store: k_new and v_new must be [b, n, Hkv, d]")
-        n = k_new.shape[1]
+        n = _i32(k_new.shape[1], "n")
         d = self._kv4_rows(cache, k_new, v_new, n)
         rc = (_lib or load()).fdl_kv4_store(self._h, ctypes.byref(d), k_new.data_ptr(),
-                                            v_new.data_ptr(), int(start), n,
+                                            v_new.data_ptr(), _i32(start, "start"), n,
                                             ctypes.byref(cache.buffers), self._at(stream))
         if rc:
             _check(rc)
@@ -485,7 +495,8 @@ class Context:
         (k, v) [b, n, Hkv, d], new tensors of `dtype` (bf16 or f32) or the given k_out and
         v_out (of one of them alone, only that one is read)."""
         self._kv4_cache(cache)
-        n = cache.seq_len - int(start) if n is None else int(n)
+        start = _i32(start, "start")
+        n = cache.seq_len - start if n is None else _i32(n, "n")
         if k_out is None and v_out is None:
             if n < 1:
                 raise ValueError(f"kv4_load: {n} rows")
@@ -495,7 +506,7 @@ class Context:
                 v_out = torch.empty_like(k_out)
         d = self._kv4_rows(cache, k_out, v_out, n)
         rc = (_lib or load()).fdl_kv4_load(
-            self._h, ctypes.byref(d), ctypes.byref(cache.buffers), int(start), n,
+            self._h, ctypes.byref(d), ctypes.byref(cache.buffers), start, n,
             None if k_out is None else k_out.data_ptr(),
             None if v_out is None else v_out.data_ptr(), self._at(stream))
         if rc:
@@ -508,8 +519,11 @@ class Context:
         if b != cache.batch or d != cache.head_dim:
             raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.batch} sequences "
                              f"and head_dim {cache.head_dim}")
-        return Kv4AttnDesc(b, Hq, cache.n_kv_heads, d, cache.seq_len, int(block_start), B,
-                           FDL_BF16, scale, window[0], window[1], sinks)
+        left, right = window
+        return Kv4AttnDesc(b, _i32(Hq, "q heads"), cache.n_kv_heads, d, cache.seq_len,
+                           _i32(block_start, "block_start"), _i32(B, "block length"), FDL_BF16,
+                           scale, _i32(left, "window"), _i32(right, "window"),
+                           _i32(sinks, "sinks"))
 
     def kv4_attention_workspace_bytes(self, desc: Kv4AttnDesc) -> int:
         return int(load().fdl_kv4_attention_workspace_bytes(self._h, ctypes.byref(desc)))

@@ -399,6 +399,8 @@ FDL_API int fdl_full_attention(fdl_ctx* ctx, const fdl_attn_desc* desc, const vo
  * infinities saturate; a NaN makes its group's scale NaN (0x7f), and the whole
  * group reads as NaN; groups whose largest value is at most 3 * 2^-9 read as 0.
  * ------------------------------------------------------------------------ */
+#define FDL_KV4_MAX_SEQ (1 << 30)   /* positions: the kernels count them in 32 bits */
+
 typedef struct {
     void* k;        /* [b, Hkv, L, d/2] uint8: codes, the even dimension of a pair in the low nibble */
     void* k_scale;  /* [b, Hkv, L, d/16] uint8: e4m3 scales */
@@ -421,7 +423,7 @@ typedef struct {
  * head; all other positions are untouched (the 4-bit form of fdl_kv_store).
  *   k_new, v_new [b, n, Hkv, d] dtype, device, 16-byte aligned, strides as in desc
  * Errors: FDL_EINVAL (shape, range, null, alignment, strides), FDL_EUNSUPPORTED
- * (head_dim; more than 32767 heads), FDL_ECUDA. */
+ * (head_dim; more than 32767 heads or FDL_KV4_MAX_SEQ positions), FDL_ECUDA. */
 FDL_API int fdl_kv4_store(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const void* k_new,
                           const void* v_new, int start, int n, const fdl_kv4_cache* cache,
                           void* stream);
@@ -472,8 +474,8 @@ FDL_API size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx,
  *   ws      device scratch of >= fdl_kv4_attention_workspace_bytes(desc) bytes,
  *           16-byte aligned (NULL where that is 16); calls that may overlap on the
  *           GPU need one each
- * Errors: FDL_EINVAL, FDL_EUNSUPPORTED (head_dim; q not bf16), FDL_EWORKSPACE,
- * FDL_ECUDA. */
+ * Errors: FDL_EINVAL, FDL_EUNSUPPORTED (head_dim; q not bf16; seq_len above
+ * FDL_KV4_MAX_SEQ; batch * Hq * B >= 2^28), FDL_EWORKSPACE, FDL_ECUDA. */
 FDL_API int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q,
                               const fdl_kv4_cache* cache, const int32_t* kv_len, void* out,
                               float* lse, void* ws, size_t ws_bytes, void* stream);

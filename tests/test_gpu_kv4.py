@@ -528,3 +528,28 @@ def test_binding_refusals(ctx):
         ctx.kv4_attention(q, c, 0, out=q)
     with pytest.raises(ValueError):
         F.Kv4Cache(c.k, c.k_scale, c.v, c.v_scale[..., :4].contiguous())
+    with pytest.raises(ValueError):
+        ctx.kv4_store(k, k, c, 1 << 32)                      # not position 0
+    with pytest.raises(ValueError):
+        ctx.kv4_load(c, 1 << 32, 5)
+
+
+@pytest.mark.parametrize("b,hq,hkv", [(24, 28, 4), (8, 32, 8)])   # alone, clusters of 2
+def test_a_wait_that_runs_out_is_reported(b, hq, hkv):
+    """Many query rows: with a limit of 1 ns every wait gives up, the kernel ends (what it has
+    issued first) and the host reads the status; a new context computes the same call."""
+    F = fdl()
+    c, q = random_cache(b, hkv, 500, 128, seed=151), queries(b, 32, hq, 128, 152)
+    x = F.Context(0)
+    x.set_wait_timeout(1)
+    x.kv4_attention(q, c, 200)
+    with pytest.raises(F.FdlError) as e:
+        x.device_status()
+    assert e.value.code == F.FDL_ETIMEOUT
+    x.close()
+    torch.cuda.synchronize()
+    x = F.Context(0)
+    out, lse = x.kv4_attention(q, c, 200, want_lse=True)
+    check_attention(q, c, out, lse, 200, seqs=range(2))
+    x.device_status()
+    x.close()

@@ -113,6 +113,7 @@ BAD_ROWS = [
     (dict(seq_len=0), EINVAL), (dict(head_dim=96), EUNSUP), (dict(head_dim=32), EUNSUP),
     (dict(dtype=2), EINVAL), (dict(row_stride=-8), EINVAL),
     (dict(row_stride=516, head_stride=128, seq_stride=51200), EINVAL),
+    (dict(seq_len=(1 << 30) + 1), EUNSUP), (dict(seq_len=2147483647), EUNSUP),
 ]
 
 
@@ -168,6 +169,7 @@ def attn(**kw):
     (dict(block_start=2147483647), EINVAL), (dict(scale=-1.0), EINVAL),
     (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
     (dict(sinks=-1), EINVAL), (dict(batch=1 << 22, n_q_heads=64), EUNSUP),
+    (dict(seq_len=(1 << 30) + 1), EUNSUP), (dict(seq_len=2147483647, block_start=2147483615), EUNSUP),
 ])
 def test_attention_refuses_bad_descriptors(kw, code):
     L = fdllm.load()
@@ -213,3 +215,22 @@ def test_binding_refuses_cpu_tensors():
     s = torch.zeros((1, 1, 4, 8), dtype=torch.uint8)
     with pytest.raises(TypeError):
         fdllm.Kv4Cache(z, s, z, s)
+
+
+def test_binding_refuses_what_ctypes_would_cut():
+    """Numbers beyond 32 bits are errors, not their lower halves."""
+    import types
+    c = types.SimpleNamespace(batch=1, n_kv_heads=2, seq_len=100, head_dim=64, device_index=0)
+    x = fdllm.Context.__new__(fdllm.Context)
+    x.device, x._h = 0, None
+    q = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
+    big = 1 << 32
+    assert x.kv4_attn_desc(q, c, 8, (3, 5), 2).window_right == 5
+    for at, window, sinks in ((big, (-1, -1), 0), (0, (big + 4, 0), 0), (0, (0, big), 0),
+                              (0, (-1, -1), big), (0, (-1, -(1 << 31) - 1), 0)):
+        with pytest.raises(ValueError):
+            x.kv4_attn_desc(q, c, at, window, sinks)
+    with pytest.raises(ValueError):
+        x.kv4_load(c, big)
+    with pytest.raises(ValueError):
+        x.kv4_load(c, 0, big + 1)
