@@ -12,7 +12,6 @@ Layouts follow include/fdllm.h:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -125,7 +124,7 @@ KV_FORMATS = {"bf16": 0, "4bit": 1}
 BATCHING = {"lockstep": 0, "compact": 1, "per_sequence": 2}
 
 
-_NO_CONTEXT = contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # none in a CPU build
 
 
 class FdlError(RuntimeError):
@@ -245,10 +244,13 @@ def rope_table(theta: float, max_pos: int, head_dim: int):
     return out
 
 
+_I32 = 1 << 31
+
+
 def _i32(x, name):
     """An int argument of a call; ctypes would drop the bits above 32."""
     x = int(x)
-    if not -(1 << 31) <= x < 1 << 31:
+    if not -_I32 <= x < _I32:
         raise ValueError(f"{name} {x} does not fit in 32 bits")
     return x
 
@@ -346,6 +348,7 @@ class Context:
         _check(L.fdl_create(ctypes.byref(h), self.device))
         self._h = h
         self._ws = None
+        self._f32 = None        # an empty f32 tensor, from which others are made
 
     def close(self):
         if getattr(self, "_h", None):
@@ -417,11 +420,6 @@ class Context:
     # -- 4-bit K/V cache ----------------------------------------------------
     # These calls are short on the GPU, so their host side is kept short too: one
     # test of everything that is usually right, and the words only when it is not.
-    def _at(self, stream):
-        """The CUDA stream handle of a call: `stream`'s, or the current one of this device."""
-        return stream.cuda_stream if stream is not None \
-            else torch._C._cuda_getCurrentRawStream(self.device)
-
     def _here(self, t, name, dtype, shape):
         """Raise unless t is a contiguous `dtype` tensor of `shape` on this device."""
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -435,21 +433,43 @@ class Context:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
-    @staticmethod
-    def _memory_of(stream):
-        """Tensors allocated inside belong to the stream of the call that writes them."""
-        return _NO_CONTEXT if stream is None else torch.cuda.stream(stream)
-
-    def _kv4_cache(self, cache):
-        if cache.device_index != self.device:
-            raise ValueError(f"the cache is on cuda:{cache.device_index}, the context on "
+    def _on(self, stream):
+        """Calls inside go to `stream`, and the tensors allocated for them belong to it."""
+        if stream.device_index != self.device:
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, the context on "
                              f"cuda:{self.device}")
+        return torch.cuda.stream(stream)
+
+    def _other_device(self, cache):
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, the context on "
+                         f"cuda:{self.device}")
 
     def _kv4_rows(self, cache, k, v, n):
         """Descriptor of unquantised rows k, v (either may be None) [b, n, Hkv, d]."""
         one = k if k is not None else v
-        want = (cache.batch, n, cache.n_kv_heads, cache.head_dim)
-        strides = None
+        b, h, d = cache.batch, cache.n_kv_heads, cache.head_dim
+        try:
+            strides, dtype = one.stride(), one.dtype
+            s0, s1, s2, s3 = strides
+            right = (s3 == 1 and one.shape == (b, n, h, d) and one.get_device() == self.device
+                     and (one is v or v is None
+                          or (v.stride() == strides and v.dtype is dtype and v.shape == one.shape
+                              and v.get_device() == self.device))
+                     and (dtype is torch.bfloat16 or dtype is torch.float32))
+        except (AttributeError, ValueError):
+            right = False
+        if not right:
+            self._refuse_rows(k, v, (b, n, h, d))
+        # a dimension of one position has no stride of its own
+        if b == 1 or n == 1 or h == 1:
+            s0, s1, s2 = (s0 if b > 1 else n * h * d, s1 if n > 1 else h * d, s2 if h > 1 else d)
+        if not (s0 or s1 or s2):
+            raise ValueError("rows without any stride are not supported")
+        return Kv4RowsDesc(b, h, d, cache.seq_len, FDL_BF16 if dtype is torch.bfloat16 else FDL_F32,
+                           s0, s1, s2)
+
+    def _refuse_rows(self, k, v, want):
+        one = k if k is not None else v
         for t, name in ((k, "k"), (v, "v")):
             if t is None:
                 continue
@@ -460,32 +480,26 @@ class Context:
                                  f"cuda:{self.device}")
             if t.shape != want:
                 raise ValueError(f"{name} rows have shape {tuple(t.shape)}, not {want}")
-            st = t.stride()
-            if st[3] != 1:
+            if t.stride(3) != 1:
                 raise ValueError(f"{name} rows must be contiguous along head_dim")
-            if strides is not None and st != strides:
-                raise ValueError("k and v rows must have the same strides")
-            strides = st
-        # a dimension of one position has no stride of its own
-        full = (n * want[2] * want[3], want[2] * want[3], want[3])
-        if want[0] == 1 or n == 1 or want[2] == 1:
-            strides = [s if size > 1 else f for s, size, f in zip(strides, want, full)]
-        if not (strides[0] or strides[1] or strides[2]):
-            raise ValueError("rows without any stride are not supported")
-        return Kv4RowsDesc(cache.batch, cache.n_kv_heads, cache.head_dim, cache.seq_len,
-                           _dtype_code(one), strides[0], strides[1], strides[2])
+        _dtype_code(one)
+        raise ValueError("k and v rows must have the same strides")
 
     def kv4_store(self, k_new, v_new, cache: Kv4Cache, start, stream=None):
         """Quantise rows k_new, v_new [b, n, Hkv, d] (bf16 or f32; any strides with head_dim
         contiguous, the same for both) into positions [start, start + n) of the cache."""
-        self._kv4_cache(cache)
+        if stream is not None:
+            with self._on(stream):
+                return self.kv4_store(k_new, v_new, cache, start)
+        if cache.device_index != self.device:
+            self._other_device(cache)
         if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4 or v_new is None:
             raise ValueError("kv4_store: k_new and v_new must be [b, n, Hkv, d]")
         n = _i32(k_new.shape[1], "n")
         d = self._kv4_rows(cache, k_new, v_new, n)
         rc = (_lib or load()).fdl_kv4_store(self._h, ctypes.byref(d), k_new.data_ptr(),
                                             v_new.data_ptr(), _i32(start, "start"), n,
-                                            ctypes.byref(cache.buffers), self._at(stream))
+                                            ctypes.byref(cache.buffers), _raw_stream(self.device))
         if rc:
             _check(rc)
 
@@ -494,21 +508,29 @@ class Context:
         """The values positions [start, start + n) of the cache stand for (n: to the end):
         (k, v) [b, n, Hkv, d], new tensors of `dtype` (bf16 or f32) or the given k_out and
         v_out (of one of them alone, only that one is read)."""
-        self._kv4_cache(cache)
+        if stream is not None:
+            with self._on(stream):
+                return self.kv4_load(cache, start, n, dtype=dtype, k_out=k_out, v_out=v_out)
+        if cache.device_index != self.device:
+            self._other_device(cache)
         start = _i32(start, "start")
         n = cache.seq_len - start if n is None else _i32(n, "n")
         if k_out is None and v_out is None:
             if n < 1:
                 raise ValueError(f"kv4_load: {n} rows")
-            with self._memory_of(stream):
-                k_out = cache.k.new_empty((cache.batch, n, cache.n_kv_heads, cache.head_dim),
-                                          dtype=dtype)
-                v_out = torch.empty_like(k_out)
-        d = self._kv4_rows(cache, k_out, v_out, n)
+            b, h, hd = cache.batch, cache.n_kv_heads, cache.head_dim
+            if dtype is not torch.bfloat16 and dtype is not torch.float32:
+                raise TypeError(f"unsupported dtype {dtype}")
+            k_out = cache.k.new_empty((b, n, h, hd), dtype=dtype)
+            v_out = torch.empty_like(k_out)
+            d = Kv4RowsDesc(b, h, hd, cache.seq_len,
+                            FDL_BF16 if dtype is torch.bfloat16 else FDL_F32, 0, 0, 0)
+        else:
+            d = self._kv4_rows(cache, k_out, v_out, n)
         rc = (_lib or load()).fdl_kv4_load(
             self._h, ctypes.byref(d), ctypes.byref(cache.buffers), start, n,
             None if k_out is None else k_out.data_ptr(),
-            None if v_out is None else v_out.data_ptr(), self._at(stream))
+            None if v_out is None else v_out.data_ptr(), _raw_stream(self.device))
         if rc:
             _check(rc)
         return k_out, v_out
@@ -520,10 +542,12 @@ class Context:
             raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.batch} sequences "
                              f"and head_dim {cache.head_dim}")
         left, right = window
-        return Kv4AttnDesc(b, _i32(Hq, "q heads"), cache.n_kv_heads, d, cache.seq_len,
-                           _i32(block_start, "block_start"), _i32(B, "block length"), FDL_BF16,
-                           scale, _i32(left, "window"), _i32(right, "window"),
-                           _i32(sinks, "sinks"))
+        if max(block_start, left, right, sinks) >= _I32 or min(block_start, left, right, sinks) < -_I32:
+            for x, name in ((block_start, "block_start"), (left, "window"), (right, "window"),
+                            (sinks, "sinks")):
+                _i32(x, name)
+        return Kv4AttnDesc(b, Hq, cache.n_kv_heads, d, cache.seq_len, int(block_start), B,
+                           FDL_BF16, scale, left, right, sinks)
 
     def kv4_attention_workspace_bytes(self, desc: Kv4AttnDesc) -> int:
         return int(load().fdl_kv4_attention_workspace_bytes(self._h, ctypes.byref(desc)))
@@ -536,7 +560,13 @@ class Context:
         positions of each sequence; window (left, right): positions around the block that it
         sees, -1 for all; sinks: first positions that stay visible. Without ws the scratch is
         allocated for the call, so calls on several streams, and captured ones, do not share it."""
-        self._kv4_cache(cache)
+        if stream is not None:
+            with self._on(stream):
+                return self.kv4_attention(q, cache, block_start, kv_len=kv_len, window=window,
+                                          sinks=sinks, out=out, lse=lse, want_lse=want_lse,
+                                          scale=scale, ws=ws)
+        if cache.device_index != self.device:
+            self._other_device(cache)
         if not isinstance(q, torch.Tensor) or q.dim() != 4:
             raise ValueError("kv4_attention: q must be [b, B, Hq, d]")
         if q.get_device() != self.device or q.dtype is not torch.bfloat16 \
@@ -551,26 +581,25 @@ class Context:
             self._here(lse, "lse", torch.float32, (d.batch, d.n_q_heads, d.block_len))
         if ws is not None:
             self._here(ws, "ws", ws.dtype, ws.shape)
-        if out is None or (lse is None and want_lse):
-            with self._memory_of(stream):
-                if out is None:
-                    out = torch.empty_like(q)
-                if lse is None and want_lse:
-                    lse = q.new_empty((d.batch, d.n_q_heads, d.block_len), dtype=torch.float32)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            if self._f32 is None:
+                self._f32 = q.new_empty(0, dtype=torch.float32)
+            lse = self._f32.new_empty((d.batch, d.n_q_heads, d.block_len))
         args = (self._h, ctypes.byref(d), q.data_ptr(), ctypes.byref(cache.buffers),
                 None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
                 None if lse is None else lse.data_ptr())
         L = _lib or load()
         if ws is None:
             # most shapes need no scratch and say so by taking none
-            rc = L.fdl_kv4_attention(*args, None, 0, self._at(stream))
+            rc = L.fdl_kv4_attention(*args, None, 0, _raw_stream(self.device))
             if rc == FDL_EWORKSPACE:
-                with self._memory_of(stream):
-                    ws = torch.empty(self.kv4_attention_workspace_bytes(d), dtype=torch.uint8,
-                                     device=q.device)
+                ws = torch.empty(self.kv4_attention_workspace_bytes(d), dtype=torch.uint8,
+                                 device=q.device)
         if ws is not None:
             rc = L.fdl_kv4_attention(*args, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     self._at(stream))
+                                     _raw_stream(self.device))
         if rc:
             _check(rc)
         return (out, lse) if (want_lse or lse is not None) else out

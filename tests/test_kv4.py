@@ -231,6 +231,14 @@ def test_binding_refuses_what_ctypes_would_cut():
         with pytest.raises(ValueError):
             x.kv4_attn_desc(q, c, at, window, sinks)
     with pytest.raises(ValueError):
+        x.kv4_attn_desc(q, c, -big)
+    with pytest.raises(ValueError):
         x.kv4_load(c, big)
     with pytest.raises(ValueError):
         x.kv4_load(c, 0, big + 1)
+    # a stream of another device
+    other = types.SimpleNamespace(device_index=1)
+    for call in (lambda: x.kv4_load(c, stream=other), lambda: x.kv4_store(q, q, c, 0, stream=other),
+                 lambda: x.kv4_attention(q, c, 0, stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
