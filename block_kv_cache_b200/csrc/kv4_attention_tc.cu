@@ -6,28 +6,39 @@
 //   S = Q K^T       Q and K in shared memory
 //   O += P V        P in TMEM, in place of the scores it came from
 // The warps divide the work by kind, a tile moving from one to the next:
-//   4 conversion warps: codes and scales from memory into registers (PF tiles
-//       ahead; positions behind the end as zeros: code 0 under scale 0), then K and
-//       V as f16 into a ring of STAGES operand tiles; a cached value is converted
-//       once per block, for all its rows
-//   2 matrix warps (one thread each, one per softmax warpgroup): tcgen05.mma as soon
-//       as the operands are there (one thread for both took 0.5 us per product
-//       of a tile and held everything else up)
+//   6 conversion warps: codes and scales from memory into registers (PF pieces of 16
+//       positions ahead; positions behind the end as zeros: code 0 under scale 0),
+//       then K and V as f16 into a ring of STAGES operand tiles; a cached value is
+//       converted once per block, for all its rows
+//   2 matrix warps, one per softmax warpgroup: tcgen05.mma as soon as the operands are
+//       there (one thread for both took 0.5 us per product of a tile and held
+//       everything else up)
 //   2 softmax warpgroups, a thread per row: each runs its own online softmax, with
 //       its own S buffers and O. With two MMA tiles a warpgroup has the rows of
 //       one; with one tile both have all rows and take every second tile of
-//       positions, and join their outputs at the end.
-// A warp's scores of the next tile are computed while it works on this one.
+//       positions, and their outputs are joined on the way out of TMEM.
+// A warp's scores of the next tile are computed while it works on this one. 16 warps,
+// so that a thread may have 128 registers; a scheduler has two softmax warps and two
+// of the others.
 //
-// What bounds it: 32 sequences, 32 queries of 28 heads on 4 kv heads of 128, 1024
-// positions: 28.2 us (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the
-// bytes). A block's 8 tiles per split take 1.1 us each: the exponentials, maxima and
-// conversions of two softmax warps per scheduler (1450 cycles when nothing else
-// issues, measured alone) beside the conversion warps. The rest is 4.7 us before the
-// first scores (start, Q) and 3.8 after the last (join, output). Searching the next
-// tile's maximum beside this one's exponentials took 29.5 us, one matrix warp for
-// both warpgroups 37.9. 8 sequences of 32 queries of 32 heads on 8 over a window of
-// 1060 positions: 18.2 us, of which the loop is a third.
+// What bounds it, in us:
+//   32 sequences, 32 queries of 28 heads on 4 kv heads of 128, 1024 positions: 24.9
+//     (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the bytes). 4.7
+//     before the first scores (launch, Q's rows, their powers of two), 16 tiles at 1.05
+//     each, 2.5 for the output. A tile: two softmax warps on a scheduler take 1450
+//     cycles when nothing else issues (measured alone), the conversion's share of
+//     it is 500 more.
+//   8 sequences, 32 queries of 32 heads on 8, a window of 1060 positions: 15.7, two
+//     blocks of 128 rows each: 4.4 before the first scores, 5.5 for 9 tiles, 5.1 for
+//     the output and the join.
+// The first and last parts run once through fresh instructions, so they are kept
+// short: a row's output leaves TMEM as bf16 and the block as one bulk copy per row (4.9
+// -> 2.5 with the stores 8 bytes per lane), and the weights of a join are found by
+// the lanes of one warp (3.0 -> 2.4; rows pushed to the block that joins them with
+// st.async: 2.6 for the pushes alone). Measured and not kept: four conversion warps
+// (28.2 and 18.2), K and V converted by different warps (26.2 and 17.3) or their
+// pieces in turn (25.7 and 16.6); the search for the next tile's maximum beside this
+// one's exponentials (1.5 more).
 //
 // Numbers as in kv4_attention.cu: f16 operands (cached values exact, queries by a
 // power of two per row), f32 scores, sums and outputs, f16 probabilities at 2^7 to
@@ -41,7 +52,7 @@ namespace fdl {
 namespace {
 
 constexpr int M4_KT = 64;                    // positions per tile
-constexpr int M4_SOFT = 8, M4_CONV = 4;      // softmax and conversion warps
+constexpr int M4_SOFT = 8, M4_CONV = 6;      // softmax and conversion warps
 constexpr int M4_MMA_WARP = M4_SOFT + M4_CONV;
 constexpr int M4_THREADS = 32 * (M4_MMA_WARP + 2);
 
@@ -95,12 +106,22 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// A run of bytes (multiples of 16) from shared to global memory, and their arrival.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, int bytes) {
+    asm volatile(
+        "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 template <int D, int MT>
 struct M4 {
     static constexpr int CB = D / 2, SB = D / KV4_GROUP;         // bytes of a cached row
     static constexpr int DC = D / 64;                            // 128-byte columns of a row
-    static constexpr int STAGES = 4;
-    static constexpr int PF = 3;                                 // tiles of codes in registers
+    static constexpr int STAGES = MT == 2 ? 4 : 5;               // of operand tiles
+    static constexpr int PF = 3;                                 // pieces of codes in registers
     static constexpr int KV = DC * M4_KT * 128;                  // an f16 K or V tile
     static constexpr int QC = 128 * 128;                         // 64 dims of 128 rows
     static constexpr int OFF_Q = 0;                              // [MT][DC][128 rows][128 B]
@@ -108,10 +129,11 @@ struct M4 {
     static constexpr int OFF_ML = OFF_V + STAGES * KV;           // float2 per row
     static constexpr int OFF_BAR = OFF_ML + 256 * 8;
     static constexpr int TOTAL = 1024 + OFF_BAR + 512;
-    // after the tiles, the output: [256][D] f32, 16-byte pieces swapped by row (with
-    // one tile of rows, of either warpgroup's positions), and weights in Q's place
-    static constexpr int OFF_O = OFF_K;
-    static_assert(256 * D * 4 <= OFF_ML - OFF_K && 8 * 256 * 4 <= MT * DC * QC, "output");
+    // after the tiles, the output in their place: bf16 rows OROW bytes apart (the next
+    // row's banks are 4 further), or, for a cluster, [128 MT][D] f32 with the 16-byte
+    // pieces swapped by row, and the rows' (max, sum) in Q's place
+    static constexpr int OFF_O = OFF_K, OROW = D * 2 + 16;
+    static_assert(MT * 128 * D * 4 <= OFF_ML - OFF_K && MT * 128 * 8 <= MT * DC * QC, "output");
     static_assert(TOTAL <= 227 * 1024, "shared memory");
     static constexpr uint32_t TMEM_O = 4 * M4_KT;                // S: [warpgroup][2] of 64
     static constexpr uint32_t TMEM = 512;
@@ -131,10 +153,8 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     const uint32_t sb = raw_at + pad;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bars = sb + S::OFF_BAR;
-    auto k_full = [&](int t) { return bars + 8 * (t % ST); };
-    auto v_full = [&](int t) { return bars + 32 + 8 * (t % ST); };
-    auto k_free = [&](int t) { return bars + 64 + 8 * (t % ST); };
-    auto v_free = [&](int t) { return bars + 96 + 8 * (t % ST); };
+    auto kv_full = [&](int t) { return bars + 8 * (t % ST); };
+    auto kv_free = [&](int t) { return bars + 64 + 8 * (t % ST); };
     auto kv_ph = [](int t) { return (uint32_t)(t / ST) & 1u; };
     // a warpgroup's j-th tile: scores there, probabilities there, O has taken them
     auto s_full = [&](int w, int j) { return bars + 128 + 16 * w + 8 * (j & 1); };
@@ -158,10 +178,8 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     if (threadIdx.x == 0) {
         FDL_TL(0, 0);
         for (int t = 0; t < ST; ++t) {
-            mbar_init(k_full(t), M4_CONV);
-            mbar_init(v_full(t), M4_CONV);
-            mbar_init(k_free(t), MT);
-            mbar_init(v_free(t), MT);
+            mbar_init(kv_full(t), 4);
+                        mbar_init(kv_free(t), MT);
         }
         for (int w = 0; w < 2; ++w)
             for (int j = 0; j < 2; ++j) {
@@ -179,6 +197,13 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // softmax warps: lane k knows where the k-th row lies that the warp fetches
+    const bf16* q_at = nullptr;
+    if (warp < M4_SOFT) {
+        constexpr int RW = MT == 2 ? 32 : 16;
+        const int r = MT == 2 ? warp * 32 + lane : (warp & 3) * 32 + (warp >> 2) * 16 + lane;
+        if (lane < RW && r < own) q_at = a.q + RowAt(a, h, row0 + r).at(a, bb, D);
+    }
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x == 0) FDL_TL(0, 1);
@@ -194,23 +219,14 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     auto tiles_of = [&](int w) { return MT == 2 ? nt : (nt + 1 - w) / 2; };
     auto tile_of = [&](int w, int j) { return MT == 2 ? j : 2 * j + w; };
     bool ok = true;
-    // four columns of a finished row, rounded once
-    auto store4 = [&](bf16* at, float4 v, float inv) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * inv, v.y * inv);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-        *reinterpret_cast<uint2*>(at) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                       *reinterpret_cast<const uint32_t*>(&hi));
-    };
-
     if (warp >= M4_SOFT && warp < M4_MMA_WARP) {
         // ------------------------------------------------------------ conversion
-        // 16 positions per warp and tile; a thread has 32 dims (16 bytes of codes,
-        // two groups) of one or two of them. Lanes are dealt so that 8 of them
-        // store to different banks.
+        // Pieces of 16 positions, four to a tile, dealt to the warps in turn; a thread
+        // has 32 dims (16 bytes of codes, two groups) of one or two of them. Lanes are
+        // dealt so that 8 of them store to different banks.
         constexpr int XN = S::DC;
-        const int cw = warp - M4_SOFT;
-        const int key0 = 16 * cw + (D == 128 ? ((lane >> 1) & 3) + 4 * (lane >> 4) : lane >> 1);
+        const int cw = warp - M4_SOFT, pieces_all = 4 * nt;
+        const int key0 = D == 128 ? ((lane >> 1) & 3) + 4 * (lane >> 4) : lane >> 1;
         const int ch = D == 128 ? (lane & 1) + 2 * ((lane >> 3) & 1) : lane & 1;
         const size_t head = ((size_t)bb * a.Hkv + h) * a.L;
         const uint8_t* kc = a.k + head * S::CB + ch * 16;
@@ -221,10 +237,10 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             uint4 k[XN], v[XN];
             uint32_t ks[XN], vs[XN];
         };
-        auto load = [&](int t, Raw& r) {
+        auto load = [&](int n, Raw& r) {     // piece n, of tile n / 4
 #pragma unroll
             for (int x = 0; x < XN; ++x) {
-                const int i = i0 + t * KT + key0 + 8 * x;
+                const int i = i0 + 16 * n + key0 + 8 * x;
                 r.k[x] = r.v[x] = make_uint4(0, 0, 0, 0);
                 r.ks[x] = r.vs[x] = 0;
                 if (i < i1) {
@@ -237,10 +253,10 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             }
         };
         // f16 tile: [64-dim column][position][128 bytes], 16-byte pieces swapped by position
-        auto convert = [&](const uint4 (&c)[XN], const uint32_t (&scale)[XN], uint32_t off) {
+        auto convert = [&](int n, const uint4 (&c)[XN], const uint32_t (&scale)[XN], uint32_t off) {
 #pragma unroll
             for (int x = 0; x < XN; ++x) {
-                const int key = key0 + 8 * x;
+                const int key = 16 * (n & 3) + key0 + 8 * x;
                 uint8_t* dst = smem + off + (ch >> 1) * (KT * 128) + key * 128;
                 const uint32_t s2 = e4m3x2_half2(scale[x]);
                 const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
@@ -256,75 +272,78 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                         make_uint4(b[0], b[1], b[2], b[3]);
                 }
             }
-            fence_proxy_async();             // the matrix instructions read it
-            __syncwarp();
         };
         Raw raw[S::PF];
 #pragma unroll
         for (int p = 0; p < S::PF; ++p)
-            if (p < nt) load(p, raw[p]);
-        for (int t0 = 0; ok && t0 < nt; t0 += S::PF) {
+            if (cw + p * M4_CONV < pieces_all) load(cw + p * M4_CONV, raw[p]);
+        for (int n0 = cw; ok && n0 < pieces_all; n0 += S::PF * M4_CONV) {
 #pragma unroll
             for (int p = 0; p < S::PF; ++p) {
-                const int t = t0 + p;
-                if (!ok || t >= nt) break;
-                if (!(ok = mbar_wait_warp(k_free(t), kv_ph(t) ^ 1u, abort_flag, a.err))) break;
-                convert(raw[p].k, raw[p].ks, S::OFF_K + (t % ST) * S::KV);
-                if (lane == 0) mbar_arrive(k_full(t));
-                if (!(ok = mbar_wait_warp(v_free(t), kv_ph(t) ^ 1u, abort_flag, a.err))) break;
-                convert(raw[p].v, raw[p].vs, S::OFF_V + (t % ST) * S::KV);
-                if (lane == 0) mbar_arrive(v_full(t));
-                if (t + S::PF < nt) load(t + S::PF, raw[p]);
+                const int n = n0 + p * M4_CONV, t = n >> 2;
+                if (!ok || n >= pieces_all) break;
+                if (!(ok = mbar_wait_warp(kv_free(t), kv_ph(t) ^ 1u, abort_flag, a.err))) break;
+                convert(n, raw[p].k, raw[p].ks, S::OFF_K + (t % ST) * S::KV);
+                convert(n, raw[p].v, raw[p].vs, S::OFF_V + (t % ST) * S::KV);
+                fence_proxy_async();         // the matrix instructions read it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv_full(t));
+                if (n + S::PF * M4_CONV < pieces_all) load(n + S::PF * M4_CONV, raw[p]);
             }
         }
     } else if (warp >= M4_MMA_WARP) {
         // ------------------------------------------------------------ products
-        const int w = warp - M4_MMA_WARP;
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, D, true);
-            const int mine = tiles_of(w);
-            // descriptors of the first k-step; the others are a few 16-byte units on
-            const uint64_t q0 = umma_desc_sw128(sb + S::OFF_Q + (MT == 2 ? w * S::DC * S::QC : 0));
-            const uint64_t k0 = umma_desc_sw128(sb + S::OFF_K);
-            const uint64_t v0 = umma_desc_sw128_mn(sb + S::OFF_V, KT * 128);
-            auto scores = [&](int j) {
-                const int t = tile_of(w, j);
-                // S buffer j & 1 holds P of tile j - 2 until O has taken it
-                ok = mbar_wait(k_full(t), kv_ph(t), abort_flag, a.err) &&
-                     mbar_wait(o_done(w, j), ph(j) ^ 1u, abort_flag, a.err);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t kt = k0 + (uint64_t)((t % ST) * (S::KV >> 4));
-                const uint32_t s_at = tmem + (2 * w + (j & 1)) * KT;
+        // The whole warp waits and counts, one lane issues: what is the same for the
+        // warp stays in uniform registers, where the instructions take their operands.
+        const int w = __shfl_sync(0xffffffffu, warp, 0) - M4_MMA_WARP;
+        constexpr uint32_t id_s = idesc_f16(128, KT, false), id_o = idesc_f16(128, D, true);
+        const int mine = tiles_of(w);
+        // descriptors of the first k-step; the others are a few 16-byte units on
+        const uint64_t q0 = umma_desc_sw128(sb + S::OFF_Q + (MT == 2 ? w * S::DC * S::QC : 0));
+        const uint64_t k0 = umma_desc_sw128(sb + S::OFF_K);
+        const uint64_t v0 = umma_desc_sw128_mn(sb + S::OFF_V, KT * 128);
+        auto scores = [&](int j) {
+            const int t = tile_of(w, j);
+            // S buffer j & 1 holds P of tile j - 2 until O has taken it
+            ok = mbar_wait_warp(kv_full(t), kv_ph(t), abort_flag, a.err) &&
+                 mbar_wait_warp(o_done(w, j), ph(j) ^ 1u, abort_flag, a.err);
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t kt = k0 + (uint64_t)((t % ST) * (S::KV >> 4));
+            const uint32_t s_at = tmem + (2 * w + (j & 1)) * KT;
+            if (lane == 0) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     umma_bf16(s_at, q0 + ((k >> 2) * (S::QC >> 4) + (k & 3) * 2),
                               kt + ((k >> 2) * (KT * 128 >> 4) + (k & 3) * 2), id_s, k > 0);
                 umma_commit(s_full(w, j));
-                umma_commit(k_free(t));
-            };
-            ok = mbar_wait(q_full, 0, abort_flag, a.err);
-            if (ok && mine > 0) scores(0);
-            for (int j = 0; ok && j < mine; ++j) {
-                if (j + 1 < mine) scores(j + 1);
-                const int t = tile_of(w, j);
-                ok = ok && mbar_wait(v_full(t), kv_ph(t), abort_flag, a.err) &&
-                     mbar_wait(p_full(w, j), ph(j), abort_flag, a.err);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vt = v0 + (uint64_t)((t % ST) * (S::KV >> 4));
-                const uint32_t p_at = tmem + (2 * w + (j & 1)) * KT;
+            }
+            __syncwarp();
+        };
+        ok = mbar_wait_warp(q_full, 0, abort_flag, a.err);
+        if (ok && mine > 0) scores(0);
+        for (int j = 0; ok && j < mine; ++j) {
+            if (j + 1 < mine) scores(j + 1);
+            const int t = tile_of(w, j);
+            ok = ok && mbar_wait_warp(p_full(w, j), ph(j), abort_flag, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vt = v0 + (uint64_t)((t % ST) * (S::KV >> 4));
+            const uint32_t p_at = tmem + (2 * w + (j & 1)) * KT;
+            if (lane == 0) {
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
                     umma_f16_ts(tmem + S::TMEM_O + w * D, p_at + k * 8, vt + k * (2048 >> 4), id_o,
                                 (j > 0 || k > 0) ? 1u : 0u);
                 umma_commit(o_done(w, j));
-                umma_commit(v_free(t));
+                umma_commit(kv_free(t));
             }
-            // whatever was issued ends before TMEM is given back
-            umma_commit(all_done);
-            mbar_wait_drain(all_done, 0, a.err);
+            __syncwarp();
         }
+        // whatever was issued ends before TMEM is given back
+        if (lane == 0) umma_commit(all_done);
+        __syncwarp();
+        mbar_wait_drain(all_done, 0, a.err);
     } else {
         // ------------------------------------------------------------ softmax
         const int w = warp >> 2, q = warp & 3;
@@ -332,8 +351,8 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         const int r = (MT == 2 ? w * 128 : 0) + lr;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
         // Q: rows into their places as they are, 16 bytes per lane; then a thread
-        // takes its row, finds its scale and stores its half of the pieces (one
-        // tile: the other warpgroup has the rest) or all, as f16 in place
+        // takes its row (one tile: every second piece, the other warpgroup has the
+        // rest), finds its scale and stores it back as f16
         float rs;
         {
             constexpr int LR = D / 8, RX = 32 / LR;              // lanes of a row, rows at once
@@ -345,15 +364,11 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             auto piece = [&](int row, int i) {
                 return reinterpret_cast<uint4*>(q_sh + place(row, i));
             };
-            // lane k knows where the warp's k-th row lies
             const int first = q * 32 + (MT == 2 ? 0 : 16 * w), i0q = lane % LR;
-            const int mine = (MT == 2 ? w * 128 : 0) + first + lane;
-            const bf16* at = mine < own && lane < RW
-                                 ? a.q + RowAt(a, h, row0 + mine).at(a, bb, D) : nullptr;
 #pragma unroll
             for (int k = 0; k < RW; k += RX) {
                 const bf16* src = reinterpret_cast<const bf16*>(__shfl_sync(
-                    0xffffffffu, reinterpret_cast<unsigned long long>(at), k + lane / LR));
+                    0xffffffffu, reinterpret_cast<unsigned long long>(q_at), k + lane / LR));
                 cp_async<16>(smem_u32(q_sh) + place(first + k + lane / LR, i0q),
                              src ? src + i0q * 8 : a.q, src != nullptr);
             }
@@ -361,30 +376,34 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             cp_wait<0>();
             if (MT == 2) __syncwarp();
             else bar_sync(1, 32 * M4_SOFT);
+            constexpr int NP = D / 8 / (3 - MT);
+            uint4 x[NP];
             uint32_t mb = 0;
-#pragma unroll 8
-            for (int i = 0; i < D / 8; ++i) {
-                const uint4 x = *piece(lr, i);
-                mb = bf16x2_max_abs(bf16x2_max_abs(mb, x.x), x.y);
-                mb = bf16x2_max_abs(bf16x2_max_abs(mb, x.z), x.w);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                x[k] = *piece(lr, MT == 2 ? k : 2 * k + w);
+                mb = bf16x2_max_abs(bf16x2_max_abs(mb, x[k].x), x[k].y);
+                mb = bf16x2_max_abs(bf16x2_max_abs(mb, x[k].z), x[k].w);
             }
             mb = bf16x2_max_bits(mb);
-            if (MT == 2) __syncwarp();
-            else bar_sync(1, 32 * M4_SOFT);
+            if constexpr (MT == 1) {
+                uint32_t* halves = reinterpret_cast<uint32_t*>(smem + S::OFF_ML);
+                halves[128 * w + lr] = mb;
+                bar_sync(1, 32 * M4_SOFT);
+                mb = max(mb, halves[128 * (w ^ 1) + lr]);
+            }
             float f, inv;
             kv4_row_scale(mb, &f, &inv);
             rs = kv4_score_scale(a.scale_log2, inv);
-#pragma unroll 4
-            for (int k = 0; k < D / 8 / (3 - MT); ++k) {
-                const int i = MT == 2 ? k : 2 * k + w;
-                const uint4 x = *piece(lr, i);
-                const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const uint32_t v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
                 uint32_t b[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
                     b[y] = pack_half2(__uint_as_float(v[y] << 16) * f,
                                       __uint_as_float(v[y] & 0xffff0000u) * f);
-                *piece(lr, i) = make_uint4(b[0], b[1], b[2], b[3]);
+                *piece(lr, MT == 2 ? k : 2 * k + w) = make_uint4(b[0], b[1], b[2], b[3]);
             }
         }
         fence_proxy_async();
@@ -465,85 +484,69 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         tc_fence_after();
         if (threadIdx.x == 0) FDL_TL(0, 5);
 
-        // ---- outputs: a thread has a row, in TMEM; through shared memory (in the
-        // tiles' place) to whole rows per warp
-        const uint32_t o_at = tmem + lanes + S::TMEM_O + w * D;
-        float4* orow = reinterpret_cast<float4*>(smem + S::OFF_O) + (w * 128 + lr) * (D / 4);
+        // ---- outputs, in TMEM: a thread takes its row, or, with one tile of rows, half
+        // of its columns, from both warpgroups' halves of the positions
         float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);
-        // a row's last word, by its thread: its maximum and sum for the other splits,
-        // or, of the only one, what its output is multiplied with
-        auto settle = [&]() {
-            if (a.cluster > 1) return make_float2(m, l);
-            if (r < own && a.lse) a.lse[RowAt(a, h, row0 + r).lse(a, bb)] = kv4_lse(m, l);
-            return make_float2(l == 0.f ? 0.f : 1.f / l, 0.f);   // nothing visible: 0
-        };
         if (MT == 1) ml[128 * w + lr] = make_float2(m, l);
         bar_sync(1, 32 * M4_SOFT);           // all tiles have been read
-        float f = 1.f;
+        float f[2] = {1.f, 1.f};             // what either half is multiplied with
         if constexpr (MT == 1) {
-            // (max, sum) of the other warpgroup's half of the positions: both halves
-            // under the common maximum
-            const float2 other = ml[128 * (w ^ 1) + lr];
-            const float mn = fmaxf(m, other.x), ms = mn == -INFINITY ? 0.f : mn;
-            f = ex2(m - ms);
-            l = l * f + other.y * ex2(other.x - ms);
-            m = mn;
+            const float2 p0 = ml[lr], p1 = ml[128 + lr];
+            m = fmaxf(p0.x, p1.x);
+            const float ms = m == -INFINITY ? 0.f : m;
+            f[0] = ex2(p0.x - ms);
+            f[1] = ex2(p1.x - ms);
+            l = p0.y * f[0] + p1.y * f[1];
         }
-#pragma unroll 4
-        for (int c = 0; c < D; c += 16) {
-            float o[16];
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = 0.f;
-            if (mine > 0) {
-                tmem_ld<16>(o_at + c, o);
-                tmem_wait_ld();
-            }
-#pragma unroll
-            for (int x = 0; x < 16; x += 4)
-                orow[((c + x) >> 2) ^ (lr & 7)] =
-                    make_float4(o[x] * f, o[x + 1] * f, o[x + 2] * f, o[x + 3] * f);
-        }
-        if (MT == 1) bar_sync(1, 32 * M4_SOFT);
-        if (MT == 2 || w == 0) ml[r] = settle();
-        if (MT == 1) bar_sync(1, 32 * M4_SOFT);
-        else __syncwarp();
-        // row k of this warp, columns [4c, 4c + 4) for lane c; both halves' sum
-        constexpr int LR = D / 4, RX = 32 / LR, RW = MT == 2 ? 32 : 16;
-        const int first = MT == 2 ? w * 128 + q * 32 : warp * 16, c = lane % LR;
-        float4* all = reinterpret_cast<float4*>(smem + S::OFF_O);
-        auto fetch = [&](int row) {
-            float4 v = all[row * (D / 4) + (c ^ (row & 7))];
-            if constexpr (MT == 1) {
-                const float4 y = all[(128 + row) * (D / 4) + (c ^ (row & 7))];
-                v.x += y.x;
-                v.y += y.y;
-                v.z += y.z;
-                v.w += y.w;
-            }
-            return v;
-        };
         if (a.cluster == 1) {
-            // lane k knows where the warp's k-th row goes
-            const int row_k = first + lane;
-            const unsigned long long at_k =
-                lane < RW && row_k < own ? reinterpret_cast<unsigned long long>(
-                                               a.out + RowAt(a, h, row0 + row_k).at(a, bb, D))
-                                         : 0;
-            const float inv_k = lane < RW ? ml[row_k].x : 0.f;
-#pragma unroll 8
-            for (int k = 0; k < RW; k += RX) {
-                const int from = k + lane / LR;
-                const unsigned long long at = __shfl_sync(0xffffffffu, at_k, from);
-                const float inv = __shfl_sync(0xffffffffu, inv_k, from);
-                const float4 v = fetch(first + from);
-                if (at) store4(reinterpret_cast<bf16*>(at) + 4 * c, v, inv);
+            const float inv = l == 0.f ? 0.f : 1.f / l;          // nothing visible: 0
+            f[0] *= inv;
+            f[1] *= inv;
+        }
+        constexpr int NC = MT == 2 ? D : D / 2;                  // columns of a thread
+        const int c0 = MT == 2 ? 0 : w * NC;
+        const uint32_t o_at = tmem + lanes + S::TMEM_O + (MT == 2 ? w * D : c0);
+#pragma unroll 2
+        for (int c = 0; c < NC; c += 16) {
+            float o[16], y[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = y[x] = 0.f;
+            // an accumulator that no tile went into holds anything
+            if (tiles_of(MT == 2 ? w : 0) > 0) tmem_ld<16>(o_at + c, o);
+            if (MT == 1 && tiles_of(1) > 0) tmem_ld<16>(o_at + D + c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = MT == 2 ? o[x] * f[0] : o[x] * f[0] + y[x] * f[1];
+            if (a.cluster == 1) {
+                uint32_t b[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const __nv_bfloat162 t = __floats2bfloat162_rn(o[2 * x], o[2 * x + 1]);
+                    b[x] = *reinterpret_cast<const uint32_t*>(&t);
+                }
+                uint4* to = reinterpret_cast<uint4*>(smem + S::OFF_O + r * S::OROW + (c0 + c) * 2);
+                to[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                to[1] = make_uint4(b[4], b[5], b[6], b[7]);
+            } else {
+                float4* to = reinterpret_cast<float4*>(smem + S::OFF_O) + r * (D / 4);
+#pragma unroll
+                for (int x = 0; x < 16; x += 4)
+                    to[((c0 + c + x) >> 2) ^ (lr & 7)] =
+                        make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
             }
-        } else if constexpr (MT == 1) {
-#pragma unroll 8
-            for (int k = 0; k < RW; k += RX) {
-                const int row = first + k + lane / LR;
-                all[row * (D / 4) + (c ^ (row & 7))] = fetch(row);
+        }
+        if (a.cluster == 1) {
+            // a row's bytes lie together here and in the output: one copy by its thread
+            fence_proxy_async();
+            if (MT == 1) bar_sync(1, 32 * M4_SOFT);
+            if ((MT == 2 || w == 0) && r < own) {
+                const RowAt row(a, h, row0 + r);
+                bulk_store(a.out + row.at(a, bb, D), sb + S::OFF_O + r * S::OROW, D * 2);
+                if (a.lse) a.lse[row.lse(a, bb)] = kv4_lse(m, l);
+                bulk_store_wait();
             }
+        } else if (MT == 2 || w == 0) {
+            reinterpret_cast<float2*>(smem + S::OFF_Q)[r] = make_float2(m, l);
         }
     }
     tc_fence_before();
@@ -554,83 +557,87 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     }
     if (a.cluster > 1) {
         // ---- several splits, joined over the cluster: rank c takes rows c, c +
-        // cluster, ... First what each split's part of them is multiplied with, a
-        // thread per row; then the rows, D / 4 lanes each, all loads of UR at once.
+        // cluster, ..., four at a time to a warp, D / 4 lanes each
         cluster_sync();
-        constexpr int LR = D / 4, RX = 32 / LR, UR = 5;
+        constexpr int LR = D / 4, RX = 32 / LR, NX = 4 / RX;     // lanes of a row, rows at once
         const int rank = split % a.cluster, c4 = lane % LR;
         const int mine_rows = (own + a.cluster - 1 - rank) / a.cluster;
-        float* wt = reinterpret_cast<float*>(smem + S::OFF_Q);   // [8][256]
-        for (int k = threadIdx.x; k < mine_rows; k += M4_THREADS) {
-            const int row = k * a.cluster + rank;
-            float2 p[8];
-            float M = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < a.cluster) p[c] = ld_cluster_f2(cluster_map(sb + S::OFF_ML + row * 8, c));
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < a.cluster) M = fmaxf(M, p[c].x);
-            const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < a.cluster) {
-                    p[c].x = ex2(p[c].x - Ms);
-                    sum += p[c].y * p[c].x;
-                }
-            float inv = 1.f;
-            if (a.parts > 1) {
-                a.part_ml[((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + row] =
-                    make_float2(M, sum);
-            } else {
-                inv = sum == 0.f ? 0.f : 1.f / sum;              // nothing visible: 0
-                if (a.lse) a.lse[RowAt(a, h, row0 + row).lse(a, bb)] = kv4_lse(M, sum);
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (c < a.cluster) wt[c * 256 + k] = p[c].x * inv;
-        }
-        __syncthreads();
-        constexpr int KX = M4_THREADS / 32 * RX;                 // rows of the block at once
-        for (int k0 = warp * RX + lane / LR; k0 < mine_rows; k0 += UR * KX) {
-            float4 acc[UR];
-#pragma unroll
-            for (int x = 0; x < UR; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < a.cluster; c += 2) {
-                float4 v[2][UR];
+        for (int kb = warp * 4; kb < mine_rows; kb += M4_THREADS / 32 * 4) {
+            // the first two splits' columns, on their way while the weights are found
+            float4 v[2][NX];
+            auto fetch = [&](int c) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int x = 0; x < UR; ++x) {
-                        const int k = k0 + x * KX, row = k * a.cluster + rank;
-                        if (c + y < a.cluster && k < mine_rows)
+                    for (int x = 0; x < NX; ++x) {
+                        const int k = kb + x * RX + lane / LR;
+                        const int row = min(k, mine_rows - 1) * a.cluster + rank;
+                        v[y][x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (c + y < a.cluster)
                             v[y][x] = ld_cluster_f4(cluster_map(
                                 sb + S::OFF_O + (row * (D / 4) + (c4 ^ (row & 7))) * 16, c + y));
                     }
+            };
+            // lane 8 i + c: what split c's part of row kb + i is multiplied with
+            const int k = kb + (lane >> 3), c = lane & 7, r = k * a.cluster + rank;
+            float2 p = make_float2(-INFINITY, 0.f);
+            if (k < mine_rows && c < a.cluster)
+                p = ld_cluster_f2(cluster_map(sb + S::OFF_Q + r * 8, c));
+            fetch(0);
+            float M = p.x;
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            float wt = ex2(p.x - (M == -INFINITY ? 0.f : M)), sum = p.y * wt;
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            unsigned long long to = 0;       // where the row goes
+            if (k < mine_rows) {
+                if (a.parts > 1) {
+                    const size_t at =
+                        ((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + r;
+                    to = reinterpret_cast<unsigned long long>(a.part + at * D);
+                    if (c == 0) a.part_ml[at] = make_float2(M, sum);
+                } else {
+                    const RowAt row(a, h, row0 + r);
+                    to = reinterpret_cast<unsigned long long>(a.out + row.at(a, bb, D));
+                    wt *= sum == 0.f ? 0.f : 1.f / sum;          // nothing visible: 0
+                    if (a.lse && c == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, sum);
+                }
+            }
+            __syncwarp();
+            float4 acc[NX];
+#pragma unroll
+            for (int x = 0; x < NX; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c0 = 0;;) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
-                    for (int x = 0; x < UR; ++x) {
-                        const int k = k0 + x * KX;
-                        if (c + y < a.cluster && k < mine_rows) {
-                            const float f = wt[(c + y) * 256 + k];
-                            acc[x].x += v[y][x].x * f;
-                            acc[x].y += v[y][x].y * f;
-                            acc[x].z += v[y][x].z * f;
-                            acc[x].w += v[y][x].w * f;
-                        }
+                    for (int x = 0; x < NX; ++x) {
+                        // of a split that is not there: 0
+                        const float f = __shfl_sync(0xffffffffu, wt,
+                                                    8 * (x * RX + lane / LR) + ((c0 + y) & 7));
+                        acc[x].x += v[y][x].x * f;
+                        acc[x].y += v[y][x].y * f;
+                        acc[x].z += v[y][x].z * f;
+                        acc[x].w += v[y][x].w * f;
                     }
+                c0 += 2;
+                if (c0 >= a.cluster) break;
+                fetch(c0);
             }
 #pragma unroll
-            for (int x = 0; x < UR; ++x) {
-                const int k = k0 + x * KX, row = k * a.cluster + rank;
-                if (k >= mine_rows) continue;
+            for (int x = 0; x < NX; ++x) {
+                const unsigned long long at =
+                    __shfl_sync(0xffffffffu, to, 8 * (x * RX + lane / LR));
+                if (!at) continue;
                 if (a.parts > 1) {
-                    const size_t at =
-                        ((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + row;
-                    *reinterpret_cast<float4*>(a.part + at * D + 4 * c4) = acc[x];
+                    reinterpret_cast<float4*>(at)[c4] = acc[x];
                 } else {
-                    store4(a.out + RowAt(a, h, row0 + row).at(a, bb, D) + 4 * c4, acc[x], 1.f);
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[x].x, acc[x].y);
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[x].z, acc[x].w);
+                    reinterpret_cast<uint2*>(at)[c4] =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                   *reinterpret_cast<const uint32_t*>(&hi));
                 }
             }
         }

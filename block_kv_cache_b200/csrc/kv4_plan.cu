@@ -106,13 +106,14 @@ int most_seen(const Kv4Attn& s) {
 Kv4Plan plan_of(const Kv4Attn& s, int sm_count) {
     Kv4Plan p;
     const int rows = s.block_len * (s.n_q_heads / s.n_kv_heads), seen = most_seen(s);
-    // The tcgen05 kernel takes 10 to 15 us before it is any faster: it is used where
-    // the 32-row blocks of the other would not all run at once (tcgen05 and the other,
-    // 64 units of 128 rows over 1024 positions: 18.0 and 29.4 us) or have much to do
-    // (32 units of 64 rows over 4096: 24.5 and 25.8; 8 units of 256 rows over 1024:
-    // 18.1 and 11.9, over 4096, just above the rule's edge: 27.8 and 25.6).
+    // The tcgen05 kernel takes 7 to 10 us before it is any faster: it is used where the
+    // 32-row blocks of the other would not all run at once (tcgen05 and the other, 64
+    // units of 128 rows over 1024 positions: 16.0 and 29.3 us) or have much to do (32
+    // units of 64 rows over 4096: 22.5 and 25.8; 32 of 128 over 1024: 13.5 and 15.4;
+    // below the edge, 8 units of 256 rows over 1024: 17.0 and 11.9; just above it, 8 of
+    // 128 over 4096: 17.6 and 16.4).
     const long long blocks = (long long)s.batch * s.n_kv_heads * ((rows + 31) / 32);
-    p.many = rows > 32 && (blocks > sm_count || blocks * seen > 1100ll * sm_count);
+    p.many = rows > 32 && (blocks > sm_count || blocks * seen > 850ll * sm_count);
     if (p.many) {
         p.chunks = (rows + 255) / 256;
         p.chunk_rows = (rows + p.chunks - 1) / p.chunks;
