@@ -95,6 +95,9 @@ def parse():
     p.add_argument("--no-cpu-baseline", action="store_true")
     p.add_argument("--e2e-loop", choices=["device", "host"], default="device",
                    help="fdl_generate's loop for the e2e decode")
+    p.add_argument("--e2e-kv", choices=["bf16", "4bit"], default="bf16",
+                   help="how the e2e decode holds the layers' K/V (4bit: lockstep, DualCache "
+                        "or PrefixCache)")
     p.add_argument("--batching", choices=["lockstep", "compact", "per_sequence"],
                    default="lockstep",
                    help="how the e2e decode moves a batch through its blocks (compact and "
@@ -505,6 +508,7 @@ def result_line(args, c, world, w, dec, toks, toks_all, kinds, step_ms, ms_max, 
                    "planted_bias": bool(args.planted_bias),
                    **({"planted_bias_hi": args.bias_hi} if args.planted_bias else {}),
                    **({"batching": args.batching} if args.batching != "lockstep" else {}),
+                   **({"e2e_kv": args.e2e_kv} if args.e2e_kv != "bf16" else {}),
                    "layers": c["layers"], "hidden": c["hidden"], "vocab": c["vocab"],
                    "parallelism": f"replicas x{world}",
                    "blocks_timed": blocks, "decode_steps_timed": nsteps,
@@ -542,7 +546,8 @@ def run_e2e(torch, ctx, w, c, args, rank):
     m = w.native()
     device_loop = args.e2e_loop == "device" and args.batching == "lockstep"
     kw = dict(block=c["block"], tau=c["tau"], cache=args.cache, bias_tok=bias[0],
-              bias_val=bias[1], device_loop=device_loop, batching=args.batching)
+              bias_val=bias[1], device_loop=device_loop, batching=args.batching,
+              kv=args.e2e_kv)
     if device_loop:
         ctx.generate(m, hp, c["gen"], **kw)           # captures and keeps the decode graph
     torch.cuda.synchronize()
@@ -561,6 +566,7 @@ def run_e2e(torch, ctx, w, c, args, rank):
             "path": f"fdl_generate (the library's decode loop, "
                     f"{'device loop: one CUDA graph per decode' if device_loop else 'host loop'}"
                     f"{'' if args.batching == 'lockstep' else ', batching ' + args.batching}"
+                    f"{'' if args.e2e_kv == 'bf16' else ', K/V in 4 bits'}"
                     f") on a host prompt: {steps} decode steps, one whole decode of {blocks} "
                     f"blocks"}
 
