@@ -797,7 +797,7 @@ size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx, const fdl_kv4_attn_
     if (!ctx) { fail(FDL_EINVAL, "kv4_attention workspace: ctx is NULL"); return 0; }
     fdl::Kv4Attn s;
     if (check_kv4_attn(desc, &s) != FDL_OK) return 0;
-    return fdl::kv4_attention_workspace_bytes(s, ctx->sm_count);
+    return fdl::kv4_attention_workspace_bytes(s, fdl::kv4_attention_plan(s, ctx->sm_count));
 }
 
 int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q,
@@ -813,16 +813,16 @@ int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q
     if (!aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3u) || ((uintptr_t)kv_len & 3u))
         return fail(FDL_EINVAL, "kv4_attention: q and out must be 16-byte aligned, lse and "
                     "kv_len 4-byte aligned");
-    const size_t need = fdl::kv4_attention_workspace_bytes(s, ctx->sm_count);
+    const fdl::Kv4Plan plan = fdl::kv4_attention_plan(s, ctx->sm_count);
+    const size_t need = fdl::kv4_attention_workspace_bytes(s, plan);
     if (need > 16 && (!ws || ws_bytes < need || !aligned16(ws)))
         return fail(FDL_EWORKSPACE, "kv4_attention: workspace needs %zu bytes (16-byte aligned), "
                     "got %zu", need, ws ? ws_bytes : (size_t)0);
     s.kv_len = kv_len;
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(FDL_ECUDA, "kv4_attention: cannot select device");
-    const cudaError_t e = fdl::launch_kv4_attention(s, q, kv4_ptrs(cache), out, lse, ws,
-                                                    ctx->sm_count, ctx->d_err,
-                                                    (cudaStream_t)stream);
+    const cudaError_t e = fdl::launch_kv4_attention(s, plan, q, kv4_ptrs(cache), out, lse,
+                                                    ws, ctx->d_err, (cudaStream_t)stream);
     return e == cudaSuccess ? FDL_OK : cuda_fail(e, "kv4_attention launch");
 }
 

@@ -118,16 +118,11 @@ __device__ __forceinline__ float kv4_lse(float m, float sum) {
 }
 
 // Few query rows per kv head (registers, mma.sync) and many (tcgen05).
-struct Kv4Plan {
-    bool many;
-    int mt;                      // 16-row (few) or 128-row (many) tiles of a chunk
-    int chunks, chunk_rows, n_splits, cluster;
-    long long units;
-};
 cudaError_t launch_kv4_attn_few(const Kv4AttnArgs& a, const Kv4Plan& p, int head_dim,
                                 cudaStream_t st);
 cudaError_t launch_kv4_attn_many(const Kv4AttnArgs& a, const Kv4Plan& p, int head_dim,
                                  cudaStream_t st);
+
 // The kernel's shared memory limit, set once per device.
 template <typename K>
 cudaError_t kv4_allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {

@@ -103,7 +103,11 @@ int most_seen(const Kv4Attn& s) {
     return s.sinks + s.win_hi - s.win_lo;
 }
 
-Kv4Plan plan_of(const Kv4Attn& s, int sm_count) {
+int parts_of(const Kv4Plan& p) { return p.n_splits / p.cluster; }
+
+}  // namespace
+
+Kv4Plan kv4_attention_plan(const Kv4Attn& s, int sm_count) {
     Kv4Plan p;
     const int rows = s.block_len * (s.n_q_heads / s.n_kv_heads), seen = most_seen(s);
     // The tcgen05 kernel takes 7 to 10 us before it is any faster: it is used where the
@@ -151,10 +155,6 @@ Kv4Plan plan_of(const Kv4Attn& s, int sm_count) {
     return p;
 }
 
-int parts_of(const Kv4Plan& p) { return p.n_splits / p.cluster; }
-
-}  // namespace
-
 int kv4_clusters(const void* kernel, int threads, size_t smem, int c, std::atomic<int>* known) {
     const int n0 = known[c].load(std::memory_order_relaxed);
     if (n0 > 0) return n0;
@@ -188,15 +188,14 @@ void kv4_attention_warm() {
             }
 }
 
-size_t kv4_attention_workspace_bytes(const Kv4Attn& s, int sm_count) {
-    const Kv4Plan p = plan_of(s, sm_count);
+size_t kv4_attention_workspace_bytes(const Kv4Attn& s, const Kv4Plan& p) {
     if (parts_of(p) == 1) return 16;
     return (size_t)p.units * parts_of(p) * p.chunk_rows * (s.head_dim * 4 + 8);
 }
 
-cudaError_t launch_kv4_attention(const Kv4Attn& s, const void* q, const Kv4Ptrs& c, void* out,
-                                 float* lse, void* ws, int sm_count, int* err, cudaStream_t st) {
-    const Kv4Plan p = plan_of(s, sm_count);
+cudaError_t launch_kv4_attention(const Kv4Attn& s, const Kv4Plan& p, const void* q,
+                                 const Kv4Ptrs& c, void* out, float* lse, void* ws, int* err,
+                                 cudaStream_t st) {
     Kv4AttnArgs a{};
     a.q = (const bf16*)q;
     a.k = c.k;

@@ -92,9 +92,17 @@ struct Kv4Attn {
 };
 // Query the cluster capacities that the plans use (outside any stream capture).
 void kv4_attention_warm();
-size_t kv4_attention_workspace_bytes(const Kv4Attn& s, int sm_count);
-cudaError_t launch_kv4_attention(const Kv4Attn& s, const void* q, const Kv4Ptrs& c, void* out,
-                                 float* lse, void* ws, int sm_count, int* dev_err,
+// Which kernel takes a call, and how it is split.
+struct Kv4Plan {
+    bool many;
+    int mt;                      // 16-row (few) or 128-row (many) tiles of a chunk
+    int chunks, chunk_rows, n_splits, cluster;
+    long long units;
+};
+Kv4Plan kv4_attention_plan(const Kv4Attn& s, int sm_count);
+size_t kv4_attention_workspace_bytes(const Kv4Attn& s, const Kv4Plan& p);
+cudaError_t launch_kv4_attention(const Kv4Attn& s, const Kv4Plan& p, const void* q,
+                                 const Kv4Ptrs& c, void* out, float* lse, void* ws, int* dev_err,
                                  cudaStream_t st);
 
 struct LMShape { int rows, hidden, vocab; };

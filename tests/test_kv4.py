@@ -222,7 +222,7 @@ def test_binding_refuses_what_ctypes_would_cut():
     import types
     c = types.SimpleNamespace(batch=1, n_kv_heads=2, seq_len=100, head_dim=64, device_index=0)
     x = fdllm.Context.__new__(fdllm.Context)
-    x.device, x._h = 0, None
+    x.device, x._h, x._kv4_descs = 0, None, {}
     q = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
     big = 1 << 32
     assert x.kv4_attn_desc(q, c, 8, (3, 5), 2).window_right == 5
