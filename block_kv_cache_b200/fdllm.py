@@ -552,12 +552,10 @@ class Context:
             raise ValueError(f"q {tuple(q.shape)} does not fit a cache of {cache.batch} sequences "
                              f"and head_dim {cache.head_dim}")
         left, right = window
-        if max(block_start, left, right, sinks) >= _I32 or min(block_start, left, right, sinks) < -_I32:
-            for x, name in ((block_start, "block_start"), (left, "window"), (right, "window"),
-                            (sinks, "sinks")):
-                _i32(x, name)
-        return Kv4AttnDesc(b, Hq, cache.n_kv_heads, d, cache.seq_len, int(block_start), B,
-                           FDL_BF16, scale, left, right, sinks)
+        return Kv4AttnDesc(b, _i32(Hq, "q heads"), cache.n_kv_heads, d, cache.seq_len,
+                           _i32(block_start, "block_start"), _i32(B, "block length"), FDL_BF16,
+                           float(scale), _i32(left, "window"), _i32(right, "window"),
+                           _i32(sinks, "sinks"))
 
     def kv4_attention_workspace_bytes(self, desc: Kv4AttnDesc) -> int:
         return int(load().fdl_kv4_attention_workspace_bytes(self._h, ctypes.byref(desc)))
