@@ -36,13 +36,15 @@
 // on a barrier. With more than 8 splits the clusters leave partial results in the
 // workspace and a second kernel joins them.
 //
-// What bounds it (heads of 128; 6.55 TB/s measured copy): one
-// token of 28 heads over 131072 positions of 4, 75.5 MB: 25.2 us with the join, in the
-// steps 5.3 TB/s with the schedulers issuing in 79 % of the cycles (conversion 2
-// cycles per 2 values and multiplication by the scale as many), 2.9 us before the
-// first step and 2.4 for the join. A 32-query block over 768 positions: 7.7 us, of
-// them 1.5 for Q, 2 for the merge. Two blocks of 8 warps per SM with up to 16 rows
-// (one: 29 us); with 32 rows the outputs take the registers of one.
+// What bounds it (heads of 128; 6.55 TB/s measured copy): one token of 28 heads over
+// 131072 positions of 4, 75.5 MB: 25.2 us with the join. 18 of them in the steps (4.2
+// TB/s), where the schedulers issue in 62 % of the cycles, the pipe that converts is
+// busy for half and the tensor pipe for 42 %: dependent work of four warps each, and
+// 128 registers allow no fifth. 2.3 before the first step, 2.4 for the join. A block of
+// 32 rows over 768 positions: 7.7 us, of them 1.5 for Q, 2.4 for the merge. Two blocks
+// of 8 warps per SM with up to 16 rows (one of 8: 29 us; one of 16: 25.2, and 26.2
+// with its warps held to within two steps of one another, so that no block is done
+// early); with 32 rows the outputs take the registers of one.
 //
 // Numbers: cached values are exact in f16 (kv4.cuh). Queries are brought to f16
 // by a power of two per row that puts the row's largest value into
