@@ -4,6 +4,8 @@
     python -m block_kv_cache_b200.kernel_cases attention --heads 32 --kv-heads 32 \
         --prefix 512 --block 32 --suffix 224 [--layers 32]
     python -m block_kv_cache_b200.kernel_cases swiglu|resid|qkv --rows 32 --n 24576 --k 4096
+    python -m block_kv_cache_b200.kernel_cases kv4attention|kv4store|kv4load [shape as for \
+        attention] [--window 512] [--sinks 4]
 
 Used to profile a single kernel (e.g. under ncu with -k/-c) and to time it
 with CUDA events. With --graph the timed calls are captured once in a CUDA
@@ -85,6 +87,43 @@ def run_attention(a, ctx):
     return {"op": "dualcache_attention", "heads": a.heads, "kv_heads": a.kv_heads, "L": L,
             "block": a.block, "batch": a.batch, "graph": a.graph, "us": us, "GBps": nbytes / us / 1e3,
             "TFLOPs": flops / us / 1e6}
+
+
+def run_kv4(a, ctx):
+    """The 4-bit cache: block attention over it, or its rows [prefix, prefix + block) stored or
+    read back; `layers` distinct caches (and, stored or read, rows) cycled."""
+    L, b, d = a.prefix + a.block + a.suffix, a.batch, a.head_dim
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def rows(n, heads):
+        return torch.randn((b, n, heads, d), generator=g, device="cuda").to(torch.bfloat16)
+    caches = []
+    for _ in range(a.layers):
+        c = fdllm.Kv4Cache.empty(b, a.kv_heads, L, d)
+        ctx.kv4_store(rows(L, a.kv_heads), rows(L, a.kv_heads), c, 0)
+        caches.append(c)
+    r = {"op": a.op, "heads": a.heads, "kv_heads": a.kv_heads, "L": L, "block": a.block,
+         "batch": b, "graph": a.graph}
+    if a.op == "kv4attention":
+        q = [rows(a.block, a.heads) for _ in range(a.layers)]
+        w = (a.window, a.window)
+        lo = 0 if a.window < 0 else max(0, a.prefix - a.window)
+        hi = L if a.window < 0 else min(L, a.prefix + a.block + a.window)
+        seen = hi - lo + min(a.sinks, lo)
+        us = _timed(a, lambda i: ctx.kv4_attention(q[i % a.layers], caches[i % a.layers], a.prefix,
+                                                   window=w, sinks=a.sinks))
+        nbytes = 2 * b * a.kv_heads * seen * d * 9 // 16 + 4 * q[0].numel()
+        r["TFLOPs"] = 4.0 * b * a.heads * a.block * seen * d / us / 1e6
+    else:
+        k, v = ([rows(a.block, a.kv_heads) for _ in range(a.layers)] for _ in range(2))
+        store = a.op == "kv4store"
+        us = _timed(a, lambda i: ctx.kv4_store(k[i % a.layers], v[i % a.layers],
+                                               caches[i % a.layers], a.prefix) if store else
+                    ctx.kv4_load(caches[i % a.layers], a.prefix, a.block, k_out=k[i % a.layers],
+                                 v_out=v[i % a.layers]))
+        nbytes = 2 * k[0].numel() * 41 // 16
+    ctx.device_status()
+    return {**r, "us": us, "GBps": nbytes / us / 1e3}
 
 
 def run_full(a, ctx):
@@ -199,6 +238,11 @@ TL_EVENTS = {
                   "split merge done", "exit"],
     "skinny": ["entry", "after dependency wait", "after prologue barrier", "first MMA issued",
                "last MMA issued", "last epilogue chunk", "-", "exit"],
+    "kv4_attention": ["entry", "after dependency wait", "Q in place", "first step's codes there",
+                      "last step", "outputs in shared memory", "exit"],
+    "kv4_attention_tc": ["entry", "after dependency wait", "Q in place", "first scores",
+                         "last probabilities", "outputs complete", "exit"],
+    "kv4_join": ["entry", "after dependency wait", "exit"],
 }
 TL_KINDS = {
     "attention": ["DualCache (no prologue)", "DualCache with the q/k/v prologue",
@@ -206,6 +250,9 @@ TL_KINDS = {
     "skinny": ["split-K sums with the RMSNorm prologue (q/k/v, gate/up)",
                "down projection with the SwiGLU prologue", "residual (O projection)",
                "split-K sums", "SwiGLU epilogue", "other"],
+    "kv4_attention": ["4-bit cache, few rows"],
+    "kv4_attention_tc": ["4-bit cache, many rows"],
+    "kv4_join": ["4-bit cache, join of the splits"],
 }
 
 
@@ -218,7 +265,7 @@ def timeline_summary():
     L = fdllm.load()
     K, C, E = 8, 512, 8
     out = {}
-    for name in ("attention", "skinny"):
+    for name in TL_EVENTS:
         fn = getattr(L, f"fdl_timeline_{name}", None)
         if fn is None:
             raise RuntimeError("not an instrumented library: set FDLLM_LIB to "
@@ -249,7 +296,7 @@ def timeline_summary():
 def main():
     p = argparse.ArgumentParser()
     p.add_argument("op", choices=["lmhead", "attention", "full", "qkvattn", "swiglu", "resid",
-                                  "qkv", "ffn"])
+                                  "qkv", "ffn", "kv4attention", "kv4store", "kv4load"])
     p.add_argument("--n", type=int, default=24576)
     p.add_argument("--k", type=int, default=4096)
     p.add_argument("--rows", type=int, default=32)
@@ -263,6 +310,9 @@ def main():
     p.add_argument("--block", type=int, default=32)
     p.add_argument("--suffix", type=int, default=224)
     p.add_argument("--layers", type=int, default=32)
+    p.add_argument("--window", type=int, default=-1,
+                   help="kv4attention: positions seen on either side of the block (-1: all)")
+    p.add_argument("--sinks", type=int, default=0, help="kv4attention: first positions seen")
     p.add_argument("--iters", type=int, default=20)
     p.add_argument("--warmup", type=int, default=3)
     p.add_argument("--graph", action="store_true", help="replay the timed calls as a CUDA graph")
@@ -276,6 +326,8 @@ def main():
         r = run_lmhead(a, ctx)
     elif a.op == "attention":
         r = run_attention(a, ctx)
+    elif a.op.startswith("kv4"):
+        r = run_kv4(a, ctx)
     elif a.op == "ffn":
         r = run_ffn(a, ctx)
     elif a.op == "full":
