@@ -22,17 +22,18 @@
 // of the others.
 //
 // What bounds it, in us:
-//   32 sequences, 32 queries of 28 heads on 4 kv heads of 128, 1024 positions: 24.9
-//     (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the bytes). 4.7
-//     before the first scores (launch, Q's rows, their powers of two), 16 tiles at 1.05
-//     each, 2.5 for the output. A tile: two softmax warps on a scheduler take 1450
+//   32 sequences, 32 queries of 28 heads on 4 kv heads of 128, 1024 positions: 24.4
+//     (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the bytes). 3.7
+//     before the first scores (Q's rows, their powers of two; 1.5 before that for the
+//     launch), 16 tiles at 1.05 each, 2.3 for the output. A tile: two softmax warps on a scheduler take 1450
 //     cycles when nothing else issues (measured alone), the conversion's share of
 //     it is 500 more.
-//   8 sequences, 32 queries of 32 heads on 8, a window of 1060 positions: 15.7, two
-//     blocks of 128 rows each: 4.4 before the first scores, 5.5 for 9 tiles, 5.1 for
+//   8 sequences, 32 queries of 32 heads on 8, a window of 1060 positions: 15.5, two
+//     blocks of 128 rows each: 3.0 before the first scores, 5.9 for 9 tiles, 5.0 for
 //     the output and the join.
 // The first and last parts run once through fresh instructions, so they are kept
-// short: a row's output leaves TMEM as bf16 and the block as one bulk copy per row (4.9
+// short: a row of Q comes as one bulk copy (16 bytes per lane with cp.async: first
+// scores 1.1 later), a row's output leaves TMEM as bf16 and the block as one bulk copy per row (4.9
 // -> 2.5 with the stores 8 bytes per lane), and the weights of a join are found by
 // the lanes of one warp (3.0 -> 2.4; rows pushed to the block that joins them with
 // st.async: 2.6 for the pushes alone). Measured and not kept: four conversion warps
@@ -112,6 +113,12 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, int bytes) {
         "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\t"
         "cp.async.bulk.commit_group;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
 }
+// From global to shared memory, counted on a barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, int bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
 __device__ __forceinline__ void bulk_store_wait() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -162,6 +169,7 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     auto o_done = [&](int w, int j) { return bars + 192 + 16 * w + 8 * (j & 1); };
     auto ph = [](int j) { return (uint32_t)(j >> 1) & 1u; };
     const uint32_t q_full = bars + 224, all_done = bars + 232;
+    auto q_in = [&](int i) { return bars + 256 + 8 * i; };       // 32 rows of Q as they are
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_BAR + 240);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -188,6 +196,7 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                 mbar_init(o_done(w, j), 1);
             }
         mbar_init(q_full, M4_SOFT);
+        for (int i = 0; i < 4 * MT; ++i) mbar_init(q_in(i), 1);
         mbar_init(all_done, 2);
         *abort_flag = 0;
         fence_barrier_init();
@@ -197,15 +206,18 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // softmax warps: lane k knows where the k-th row lies that the warp fetches
+    // where the row of Q lies that this thread fetches
     const bf16* q_at = nullptr;
-    if (warp < M4_SOFT) {
-        constexpr int RW = MT == 2 ? 32 : 16;
-        const int r = MT == 2 ? warp * 32 + lane : (warp & 3) * 32 + (warp >> 2) * 16 + lane;
-        if (lane < RW && r < own) q_at = a.q + RowAt(a, h, row0 + r).at(a, bb, D);
-    }
+    if (warp < 4 * MT && warp * 32 + lane < own)
+        q_at = a.q + RowAt(a, h, row0 + warp * 32 + lane).at(a, bb, D);
     pdl_wait();
     pdl_trigger();
+    if (warp < 4 * MT) {
+        if (lane == 0) mbar_arrive_expect_tx(q_in(warp), max(0, min(32, own - warp * 32)) * D * 2);
+        __syncwarp();
+        if (q_at)
+            bulk_load(sb + S::OFF_Q + (warp * 32 + lane) * (D * 2), q_at, D * 2, q_in(warp));
+    }
     if (threadIdx.x == 0) FDL_TL(0, 1);
 
     const Seen seen(a, bb);
@@ -350,38 +362,29 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         const int lr = q * 32 + lane;                            // lane of the MMA tile
         const int r = (MT == 2 ? w * 128 : 0) + lr;
         const uint32_t lanes = (uint32_t)(q * 32) << 16;
-        // Q: rows into their places as they are, 16 bytes per lane; then a thread
-        // takes its row (one tile: every second piece, the other warpgroup has the
-        // rest), finds its scale and stores it back as f16
+        // Q: its rows are on their way, one after the other, into their place; a thread
+        // takes its row (one tile: half of it, the other warpgroup has the rest) into
+        // registers, finds its scale and stores it back as f16, in the 16-byte pieces
+        // that the matrix instructions want swapped by row. The piece that lane l takes
+        // k-th, k ^ 2 l in the field of 8 elements, makes both the reads (at a distance
+        // of whole rows) and the writes (k ^ 2 l ^ l = k ^ 3 l) hit different banks.
         float rs;
         {
-            constexpr int LR = D / 8, RX = 32 / LR;              // lanes of a row, rows at once
-            constexpr int RW = MT == 2 ? 32 : 16;                // rows that this warp fetches
             uint8_t* q_sh = smem + S::OFF_Q + (MT == 2 ? w * S::DC * S::QC : 0);
-            auto place = [&](int row, int i) {
-                return (i >> 3) * S::QC + row * 128 + (((i & 7) ^ (row & 7)) << 4);
-            };
-            auto piece = [&](int row, int i) {
-                return reinterpret_cast<uint4*>(q_sh + place(row, i));
-            };
-            const int first = q * 32 + (MT == 2 ? 0 : 16 * w), i0q = lane % LR;
-#pragma unroll
-            for (int k = 0; k < RW; k += RX) {
-                const bf16* src = reinterpret_cast<const bf16*>(__shfl_sync(
-                    0xffffffffu, reinterpret_cast<unsigned long long>(q_at), k + lane / LR));
-                cp_async<16>(smem_u32(q_sh) + place(first + k + lane / LR, i0q),
-                             src ? src + i0q * 8 : a.q, src != nullptr);
-            }
-            cp_commit();
-            cp_wait<0>();
-            if (MT == 2) __syncwarp();
-            else bar_sync(1, 32 * M4_SOFT);
             constexpr int NP = D / 8 / (3 - MT);
+            const int l2 = ((lane << 1) ^ ((lane >> 2 & 1) * 11)) & 7;
+            auto piece = [&](int k) {
+                return (MT == 2 ? 0 : w * NP) + ((k & ~7) | (((k & 7) ^ l2) & (NP - 1)));
+            };
             uint4 x[NP];
             uint32_t mb = 0;
+            ok = mbar_wait_drain(q_in(MT == 2 ? warp : q), 0, a.err);
+            ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
-                x[k] = *piece(lr, MT == 2 ? k : 2 * k + w);
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (r < own)
+                    x[k] = *reinterpret_cast<const uint4*>(q_sh + lr * (D * 2) + piece(k) * 16);
                 mb = bf16x2_max_abs(bf16x2_max_abs(mb, x[k].x), x[k].y);
                 mb = bf16x2_max_abs(bf16x2_max_abs(mb, x[k].z), x[k].w);
             }
@@ -391,6 +394,8 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                 halves[128 * w + lr] = mb;
                 bar_sync(1, 32 * M4_SOFT);
                 mb = max(mb, halves[128 * (w ^ 1) + lr]);
+            } else {
+                bar_sync(2 + w, 128);        // the warpgroup has read its rows
             }
             float f, inv;
             kv4_row_scale(mb, &f, &inv);
@@ -403,7 +408,10 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                 for (int y = 0; y < 4; ++y)
                     b[y] = pack_half2(__uint_as_float(v[y] << 16) * f,
                                       __uint_as_float(v[y] & 0xffff0000u) * f);
-                *piece(lr, MT == 2 ? k : 2 * k + w) = make_uint4(b[0], b[1], b[2], b[3]);
+                const int p = piece(k);
+                *reinterpret_cast<uint4*>(q_sh + (p >> 3) * S::QC + lr * 128 +
+                                          (((p & 7) ^ (lr & 7)) << 4)) =
+                    make_uint4(b[0], b[1], b[2], b[3]);
             }
         }
         fence_proxy_async();
@@ -415,7 +423,7 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         const int mine = tiles_of(w);
         // warps whose rows are all padding only keep the barriers going
         const bool live = (MT == 2 ? w * 128 : 0) + q * 32 < own;
-        for (int j = 0; j < mine; ++j) {
+        for (int j = 0; ok && j < mine; ++j) {
             if (!(ok = mbar_wait_warp(s_full(w, j), ph(j), abort_flag, a.err))) break;
             tc_fence_after();
             if (j == 0 && threadIdx.x == 0) FDL_TL(0, 3);
