@@ -371,8 +371,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
 #pragma unroll
                 for (int nt = 0; nt < S::NT; ++nt)
                     v = fmaxf(v, fmaxf(s[mt][nt][2 * x], s[mt][nt][2 * x + 1]));
-                mx[mt][x] = v * rs[mt][x];   // rs >= 0 commutes with the maximum
-                grow |= mx[mt][x] > m[mt][x] + 8.f;
+                mx[mt][x] = v;
+                grow |= (v - m[mt][x]) * rs[mt][x] > 8.f;
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -384,7 +384,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                     v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
                     const float mn = fmaxf(m[mt][x], v);
                     // nothing seen so far: l and o are zero and stay so
-                    const float alpha = mn == -INFINITY ? 1.f : ex2(m[mt][x] - mn);
+                    const float alpha =
+                        mn == -INFINITY ? 1.f : kv4_weight(m[mt][x], mn, rs[mt][x]);
                     m[mt][x] = mn;
                     l[mt][x] *= alpha;
 #pragma unroll
@@ -399,11 +400,12 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float nm = m[mt][x] == -INFINITY ? 0.f : KV4_SHIFT - m[mt][x];
+                const float base_m = kv4_base(m[mt][x]);
 #pragma unroll
                 for (int nt = 0; nt < S::NT; ++nt) {
-                    const float p0 = ex2(fmaf(s[mt][nt][2 * x], rs[mt][x], nm));
-                    const float p1 = ex2(fmaf(s[mt][nt][2 * x + 1], rs[mt][x], nm));
+                    const float2 e = kv4_exponents(s[mt][nt][2 * x], s[mt][nt][2 * x + 1], base_m,
+                                                   rs[mt][x]);
+                    const float p0 = ex2(e.x), p1 = ex2(e.y);
                     l[mt][x] += p0 + p1;
                     p[mt][nt][x] = pack_half2(p0, p1);
                 }
@@ -495,12 +497,13 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
     if (a.cluster > 1) sm100::cluster_wait();
     __syncthreads();
     if (threadIdx.x == 0) FDL_TL(0, 5);
+    const float* row_scale = reinterpret_cast<const float*>(smem + S::OFF_RS);
     // row r, columns [4c, 4c + 4): out, to the workspace, or to the block that joins r
     auto finish = [&](int r, int c, float4 v, float M, float sum) {
         if (a.parts > 1) {
             const size_t at = ((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + r;
             *reinterpret_cast<float4*>(a.part + at * D + 4 * c) = v;
-            if (c == 0) a.part_ml[at] = make_float2(M, sum);
+            if (c == 0) a.part_ml[at] = make_float4(M, sum, row_scale[r], 0.f);
             return;
         }
         const RowAt row(a, h, row0 + r);
@@ -509,7 +512,7 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
         __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * inv, v.w * inv);
         *reinterpret_cast<uint2*>(a.out + row.at(a, bb, D) + 4 * c) =
             make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-        if (a.lse && c == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, sum);
+        if (a.lse && c == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, row_scale[r], sum);
     };
     for (int it = threadIdx.x; it < own * (D / 4); it += A4_THREADS) {
         const int r = it / (D / 4), c = it % (D / 4);
@@ -526,11 +529,11 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                     (size_t)(w * S::ROWS + r) * S::PROW)[slot(c)];
             M = fmaxf(M, p[w].x);
         }
-        const float Ms = M == -INFINITY ? 0.f : M;
+        const float Ms = kv4_base(M), scale = row_scale[r];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < A4_WARPS; ++w) {
-            const float f = ex2(p[w].x - Ms);
+            const float f = kv4_weight(p[w].x, Ms, scale);
             sum += p[w].y * f;
             acc.x += v[w].x * f;
             acc.y += v[w].y * f;
@@ -552,7 +555,7 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
         // way out of a wait that ran out too, nothing may land in a block that left.
         const bool got = sm100::mbar_wait_drain(bar, 0, a.err);
         for (int it = threadIdx.x; got && it < mine_rows * (D / 4); it += A4_THREADS) {
-            const int k = it / (D / 4), c = it % (D / 4);
+            const int k = it / (D / 4), c = it % (D / 4), r = k * a.cluster + rank;
             float M = -INFINITY, sum = 0.f;
             float2 p[A4_CLUSTER];
             float4 v[A4_CLUSTER];
@@ -564,19 +567,19 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                     v[x] = reinterpret_cast<const float4*>(row)[c];
                     M = fmaxf(M, p[x].x);
                 }
-            const float Ms = M == -INFINITY ? 0.f : M;
+            const float Ms = kv4_base(M), scale = row_scale[r];
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int x = 0; x < A4_CLUSTER; ++x)
                 if (x < a.cluster) {
-                    const float f = ex2(p[x].x - Ms);
+                    const float f = kv4_weight(p[x].x, Ms, scale);
                     sum += p[x].y * f;
                     acc.x += v[x].x * f;
                     acc.y += v[x].y * f;
                     acc.z += v[x].z * f;
                     acc.w += v[x].w * f;
                 }
-            finish(k * a.cluster + rank, c, acc, M, sum);
+            finish(r, c, acc, M, sum);
         }
     }
     if (threadIdx.x == 0) FDL_TL(0, 6);

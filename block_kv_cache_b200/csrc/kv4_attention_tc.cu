@@ -138,9 +138,9 @@ struct M4 {
     static constexpr int TOTAL = 1024 + OFF_BAR + 512;
     // after the tiles, the output in their place: bf16 rows OROW bytes apart (the next
     // row's banks are 4 further), or, for a cluster, [128 MT][D] f32 with the 16-byte
-    // pieces swapped by row, and the rows' (max, sum) in Q's place
+    // pieces swapped by row, and the rows' (max, sum, score scale) in Q's place
     static constexpr int OFF_O = OFF_K, OROW = D * 2 + 16;
-    static_assert(MT * 128 * D * 4 <= OFF_ML - OFF_K && MT * 128 * 8 <= MT * DC * QC, "output");
+    static_assert(MT * 128 * D * 4 <= OFF_ML - OFF_K && MT * 128 * 16 <= MT * DC * QC, "output");
     static_assert(TOTAL <= 227 * 1024, "shared memory");
     static constexpr uint32_t TMEM_O = 4 * M4_KT;                // S: [warpgroup][2] of 64
     static constexpr uint32_t TMEM = 512;
@@ -419,7 +419,7 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         if (lane == 0) mbar_arrive(q_full);
         if (threadIdx.x == 0) FDL_TL(0, 2);
 
-        float m = -INFINITY, l = 0.f;                            // log2 units
+        float m = -INFINITY, l = 0.f;
         const int mine = tiles_of(w);
         // warps whose rows are all padding only keep the barriers going
         const bool live = (MT == 2 ? w * 128 : 0) + q * 32 < own;
@@ -441,11 +441,11 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int c = 4; c < KT; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * rs;
-                if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                if (__any_sync(0xffffffffu, (mx - m) * rs > 8.f)) {
                     const float mn = fmaxf(m, mx);
                     // nothing seen so far: l and O are zero and stay so
-                    const float alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+                    const float alpha = mn == -INFINITY ? 1.f : kv4_weight(m, mn, rs);
                     m = mn;
                     l *= alpha;
                     if (j > 0) {
@@ -464,15 +464,15 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                         }
                     }
                 }
-                const float nm = m == -INFINITY ? 0.f : KV4_SHIFT - m;
+                const float base_m = kv4_base(m);
                 float l2[2] = {0.f, 0.f};
 #pragma unroll
                 for (int c0 = 0; c0 < KT; c0 += 32) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float p0 = ex2(fmaf(s[c0 + c], rs, nm));
-                        const float p1 = ex2(fmaf(s[c0 + c + 1], rs, nm));
+                        const float2 e = kv4_exponents(s[c0 + c], s[c0 + c + 1], base_m, rs);
+                        const float p0 = ex2(e.x), p1 = ex2(e.y);
                         l2[0] += p0;
                         l2[1] += p1;
                         pk[c >> 1] = pack_half2(p0, p1);
@@ -501,9 +501,9 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         if constexpr (MT == 1) {
             const float2 p0 = ml[lr], p1 = ml[128 + lr];
             m = fmaxf(p0.x, p1.x);
-            const float ms = m == -INFINITY ? 0.f : m;
-            f[0] = ex2(p0.x - ms);
-            f[1] = ex2(p1.x - ms);
+            const float ms = kv4_base(m);
+            f[0] = kv4_weight(p0.x, ms, rs);
+            f[1] = kv4_weight(p1.x, ms, rs);
             l = p0.y * f[0] + p1.y * f[1];
         }
         if (a.cluster == 1) {
@@ -550,11 +550,11 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             if ((MT == 2 || w == 0) && r < own) {
                 const RowAt row(a, h, row0 + r);
                 bulk_store(a.out + row.at(a, bb, D), sb + S::OFF_O + r * S::OROW, D * 2);
-                if (a.lse) a.lse[row.lse(a, bb)] = kv4_lse(m, l);
+                if (a.lse) a.lse[row.lse(a, bb)] = kv4_lse(m, rs, l);
                 bulk_store_wait();
             }
         } else if (MT == 2 || w == 0) {
-            reinterpret_cast<float2*>(smem + S::OFF_Q)[r] = make_float2(m, l);
+            reinterpret_cast<float4*>(smem + S::OFF_Q)[r] = make_float4(m, l, rs, 0.f);
         }
     }
     tc_fence_before();
@@ -588,14 +588,15 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
             };
             // lane 8 i + c: what split c's part of row kb + i is multiplied with
             const int k = kb + (lane >> 3), c = lane & 7, r = k * a.cluster + rank;
-            float2 p = make_float2(-INFINITY, 0.f);
+            float4 p = make_float4(-INFINITY, 0.f, 0.f, 0.f);
             if (k < mine_rows && c < a.cluster)
-                p = ld_cluster_f2(cluster_map(sb + S::OFF_Q + r * 8, c));
+                p = ld_cluster_f4(cluster_map(sb + S::OFF_Q + r * 16, c));
             fetch(0);
             float M = p.x;
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float wt = ex2(p.x - (M == -INFINITY ? 0.f : M)), sum = p.y * wt;
+            // of a split that is not there: 0
+            float wt = c < a.cluster ? kv4_weight(p.x, kv4_base(M), p.z) : 0.f, sum = p.y * wt;
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             unsigned long long to = 0;       // where the row goes
@@ -604,12 +605,12 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
                     const size_t at =
                         ((size_t)unit * a.parts + split / a.cluster) * a.chunk_rows + r;
                     to = reinterpret_cast<unsigned long long>(a.part + at * D);
-                    if (c == 0) a.part_ml[at] = make_float2(M, sum);
+                    if (c == 0) a.part_ml[at] = make_float4(M, sum, p.z, 0.f);
                 } else {
                     const RowAt row(a, h, row0 + r);
                     to = reinterpret_cast<unsigned long long>(a.out + row.at(a, bb, D));
                     wt *= sum == 0.f ? 0.f : 1.f / sum;          // nothing visible: 0
-                    if (a.lse && c == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, sum);
+                    if (a.lse && c == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, p.z, sum);
                 }
             }
             __syncwarp();

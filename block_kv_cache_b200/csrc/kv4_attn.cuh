@@ -16,7 +16,7 @@ struct Kv4AttnArgs {
     bf16* out;
     float* lse;                  // optional
     float* part;                 // [unit][part][chunk_rows][D], with several parts
-    float2* part_ml;             // [unit][part][chunk_rows]: running maximum, sum
+    float4* part_ml;             // [unit][part][chunk_rows]: running maximum, sum, score scale
     const int32_t* kv_len;       // optional
     int B, Hq, Hkv, G, L;
     FastDiv by_g;
@@ -106,15 +106,40 @@ __device__ __forceinline__ void kv4_row_scale(uint32_t max_bits, float* f, float
     }
 }
 
-// What a row's scores are multiplied with: at least the smallest normal number,
-// so that a score of -inf stays one.
+// What a row's scores are multiplied with (rs below): at least the smallest normal
+// number, so that a score of -inf stays one, and finite, so that a difference of 0
+// stays one.
 __device__ __forceinline__ float kv4_score_scale(float scale_log2, float inv) {
-    return fmaxf(scale_log2 * inv, 1.2e-38f);
+    return fminf(fmaxf(scale_log2 * inv, 1.2e-38f), 3.4028234663852886e38f);
 }
 
-// The log-sum-exp of a row from its maximum (log2 units) and sum.
-__device__ __forceinline__ float kv4_lse(float m, float sum) {
-    return ((m == -INFINITY ? 0.f : m) - KV4_SHIFT + log2f(sum)) * 0.69314718055994530942f;
+// Maxima are kept in the scores' own units, and every exponent is a difference of two
+// scores times rs: with a product m * rs that is rounded before the subtraction, the
+// maximum's own exponent would be off by half an ulp of m * rs, which leaves f16's
+// range where |m * rs| passes 2^27. Nothing seen (m = -inf) gives 2^-inf = 0.
+__device__ __forceinline__ float kv4_base(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ float kv4_weight(float m, float base, float rs) {
+    return ex2((m - base) * rs);
+}
+// log2 of two probabilities, (s - base) * rs + shift.
+__device__ __forceinline__ float2 kv4_exponents(float s0, float s1, float base, float rs) {
+    float2 r;
+    asm("{\n\t.reg .b64 s, b, f, k;\n\t"
+        "mov.b64 s, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %4};\n\t"
+        "mov.b64 f, {%5, %5};\n\t"
+        "mov.b64 k, {%6, %6};\n\t"
+        "add.rn.f32x2 s, s, b;\n\t"
+        "fma.rn.f32x2 s, s, f, k;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(s0), "f"(s1), "f"(-base), "f"(rs), "f"(KV4_SHIFT));
+    return r;
+}
+
+// The log-sum-exp of a row from its maximum and sum.
+__device__ __forceinline__ float kv4_lse(float m, float rs, float sum) {
+    return fmaf(kv4_base(m), rs, log2f(sum) - KV4_SHIFT) * 0.69314718055994530942f;
 }
 
 // Few query rows per kv head (registers, mma.sync) and many (tcgen05).

@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const Kv4Attn
     float acc[E], M = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int x = 0; x < E; ++x) acc[x] = 0.f;
+    const float rs = a.part_ml[at].z;
     for (int s0 = warp; s0 < a.parts; s0 += U * JOIN_WARPS) {
         float2 p[U];
         float v[U][E];
@@ -41,7 +42,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const Kv4Attn
             for (int x = 0; x < E; ++x) v[k][x] = 0.f;
             if (s < a.parts) {
                 const size_t i = at + (size_t)s * a.chunk_rows;
-                p[k] = a.part_ml[i];
+                p[k] = *reinterpret_cast<const float2*>(a.part_ml + i);
                 const float2* src = reinterpret_cast<const float2*>(a.part + i * D + lane * E);
 #pragma unroll
                 for (int x = 0; x < E; x += 2) {
@@ -54,13 +55,13 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const Kv4Attn
         float mn = M;
 #pragma unroll
         for (int k = 0; k < U; ++k) mn = fmaxf(mn, p[k].x);
-        const float ms = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ms);
+        const float ms = kv4_base(mn), f0 = kv4_weight(M, ms, rs);
         sum *= f0;
 #pragma unroll
         for (int x = 0; x < E; ++x) acc[x] *= f0;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const float f = ex2(p[k].x - ms);
+            const float f = kv4_weight(p[k].x, ms, rs);
             sum += p[k].y * f;
 #pragma unroll
             for (int x = 0; x < E; ++x) acc[x] += v[k][x] * f;
@@ -79,12 +80,12 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const Kv4Attn
         w8[w] = ml[w];
         M = fmaxf(M, w8[w].x);
     }
-    const float Ms = M == -INFINITY ? 0.f : M;
+    const float Ms = kv4_base(M);
     float o0 = 0.f, o1 = 0.f;
     sum = 0.f;
 #pragma unroll
     for (int w = 0; w < JOIN_WARPS; ++w) {
-        const float f = ex2(w8[w].x - Ms);
+        const float f = kv4_weight(w8[w].x, Ms, rs);
         o0 += part[w][2 * threadIdx.x] * f;
         o1 += part[w][2 * threadIdx.x + 1] * f;
         sum += w8[w].y * f;
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const Kv4Attn
     const float inv = sum == 0.f ? 0.f : 1.f / sum;              // nothing visible: 0
     *reinterpret_cast<__nv_bfloat162*>(a.out + row.at(a, bb, D) + 2 * threadIdx.x) =
         __floats2bfloat162_rn(o0 * inv, o1 * inv);
-    if (a.lse && threadIdx.x == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, sum);
+    if (a.lse && threadIdx.x == 0) a.lse[row.lse(a, bb)] = kv4_lse(M, rs, sum);
     if (threadIdx.x == 0) FDL_TL(0, 2);
 }
 
@@ -190,7 +191,7 @@ void kv4_attention_warm() {
 
 size_t kv4_attention_workspace_bytes(const Kv4Attn& s, const Kv4Plan& p) {
     if (parts_of(p) == 1) return 16;
-    return (size_t)p.units * parts_of(p) * p.chunk_rows * (s.head_dim * 4 + 8);
+    return (size_t)p.units * parts_of(p) * p.chunk_rows * (s.head_dim * 4 + 16);
 }
 
 cudaError_t launch_kv4_attention(const Kv4Attn& s, const Kv4Plan& p, const void* q,
@@ -220,10 +221,10 @@ cudaError_t launch_kv4_attention(const Kv4Attn& s, const Kv4Plan& p, const void*
     a.sinks = s.sinks;
     a.win_lo = s.win_lo;
     a.win_hi = s.win_hi;
-    a.scale_log2 = s.scale * 1.4426950408889634f;
+    a.scale_log2 = fminf(s.scale * 1.4426950408889634f, 3.4028234663852886e38f);
     a.err = err;
     a.part = (float*)ws;
-    a.part_ml = (float2*)((float*)ws + (size_t)p.units * a.parts * a.chunk_rows * s.head_dim);
+    a.part_ml = (float4*)((float*)ws + (size_t)p.units * a.parts * a.chunk_rows * s.head_dim);
     cudaError_t e = p.many ? launch_kv4_attn_many(a, p, s.head_dim, st)
                            : launch_kv4_attn_few(a, p, s.head_dim, st);
     if (e != cudaSuccess || a.parts == 1) return e;

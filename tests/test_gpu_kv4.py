@@ -563,3 +563,68 @@ def test_a_wait_that_runs_out_is_reported(b, hq, hkv):
     check_attention(q, c, out, lse, 200, seqs=range(2))
     x.device_status()
     x.close()
+
+
+# ------------------------------------------------------- scores of any finite size
+EXACT_SHAPES = [  # b, Hq, Hkv, d, L, start, B
+    (1, 4, 4, 128, 300, 100, 32),        # few rows, joined over a cluster
+    (2, 6, 3, 64, 333, 0, 9),
+    (1, 7, 1, 128, 5000, 4999, 1),       # ... and in the workspace
+    (24, 28, 4, 128, 200, 100, 32),      # many rows: two tiles, one block
+    (8, 32, 8, 128, 500, 200, 32),       # one tile, a cluster of 2
+    (38, 32, 8, 64, 90, 20, 32),         # one tile, one block
+    (2, 32, 8, 128, 2300, 1000, 32),     # ... and in the workspace
+]
+
+
+def exact_scores(b, hq, hkv, d, L, B, seed, power):
+    """Keys that are multiples of 0.5 up to 6 and queries that are whole numbers up to 8 times
+    2^power: every partial sum of a score is a multiple of half that power below 2^14 of it, so
+    f32 holds it whatever the order."""
+    rng = np.random.default_rng(seed)
+    codes = rng.integers(0, 256, (2, b, hkv, L, d // 2), dtype=np.uint8)
+    scales = np.full((2, b, hkv, L, d // 16), 0x38, np.uint8)               # 1.0
+    c = fdl().Kv4Cache(*(torch.from_numpy(x).cuda()
+                         for x in (codes[0], scales[0], codes[1], scales[1])))
+    q = torch.from_numpy(rng.integers(-8, 9, (b, B, hq, d)) * 2.0 ** power).to(torch.bfloat16).cuda()
+    return c, q
+
+
+def check_exact_scores(q, cache, out, lse, scale=None):
+    """As check_attention with dz = 0: a score's error is none. The exponents are (s - max) rs in
+    f32, a gap g off by at most 2^-21 g (the factors' roundings and the product's), which moves a
+    probability by 2^-21 g e^-g < 2^-22, as its ex2.approx does. The log-sum-exp's own size passes
+    f32's before the output does: it is infinite there."""
+    kc, ks, vc, vs = host(cache)
+    b, B, hq, d = q.shape
+    qn, on, ln = q.double().cpu().numpy(), out.double().cpu().numpy(), lse.double().cpu().numpy()
+    n = cache.seq_len
+    for i in range(min(b, 2)):
+        k, v = O.kv4_values(kc[i], ks[i]), O.kv4_values(vc[i], vs[i])
+        ref, rl, spread = O.kv4_attention(qn[i], k, v, np.ones(n, bool), scale)
+        grid = np.repeat(np.abs(v).sum(1), hq // cache.n_kv_heads, 0) * 2.0 ** -32 + 2.0 ** -133
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + n * 2.0 ** -22) * spread + grid
+        assert np.isfinite(on[i]).all()
+        assert (np.abs(on[i] - ref) <= tol).all(), (i, np.abs(on[i] - ref).max())
+        top = 2.0 ** 128
+        sure = np.abs(rl) < top * (1 - 2.0 ** -20)
+        assert (np.abs(ln[i] - rl)[sure] <= (n * 2.0 ** -23 + 2.0 ** -20 * (1 + np.abs(rl)))[sure]).all()
+        assert (np.abs(ln[i])[np.abs(rl) > top * (1 + 2.0 ** -20)] == np.inf).all()
+
+
+@pytest.mark.parametrize("power", [-120, 0, 20, 27, 30, 60, 110, 124])
+@pytest.mark.parametrize("b,hq,hkv,d,L,start,B", EXACT_SHAPES)
+def test_attention_of_exact_scores(ctx, b, hq, hkv, d, L, start, B, power):
+    """Uniform to one-hot rows, with ties, whatever the scores' size."""
+    c, q = exact_scores(b, hq, hkv, d, L, B, 161, power)
+    out, lse = ctx.kv4_attention(q, c, start, want_lse=True)
+    ctx.device_status()
+    check_exact_scores(q, c, out, lse)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e30, 3.4e38])
+@pytest.mark.parametrize("b,hq,hkv,d,L,start,B", EXACT_SHAPES[2:5])
+def test_attention_of_exact_scores_under_any_scale(ctx, b, hq, hkv, d, L, start, B, scale):
+    c, q = exact_scores(b, hq, hkv, d, L, B, 162, 0)
+    out, lse = ctx.kv4_attention(q, c, start, want_lse=True, scale=scale)
+    check_exact_scores(q, c, out, lse, float(np.float32(scale)))
