@@ -581,7 +581,10 @@ class Context:
                 or not q.is_contiguous():
             self._here(q, "q", torch.bfloat16, q.shape)
         b, B, Hq, hd = q.shape
+        # numbers before they become a key: a tensor would be one by its identity, whatever
+        # it holds by the next call
         left, right = window
+        left, right, sinks, scale = int(left), int(right), int(sinks), float(scale)
         block_start = int(block_start)
         key = (b, B, Hq, hd, cache.batch, cache.n_kv_heads, cache.seq_len, cache.head_dim,
                block_start, left, right, sinks, scale)
@@ -590,7 +593,7 @@ class Context:
             if len(self._kv4_descs) >= 4096:
                 self._kv4_descs.clear()
             d = self._kv4_descs[key] = ctypes.byref(
-                self.kv4_attn_desc(q, cache, block_start, window, sinks, scale))
+                self.kv4_attn_desc(q, cache, block_start, (left, right), sinks, scale))
         if kv_len is not None:
             self._here(kv_len, "kv_len", torch.int32, (b,))
         if out is None:

@@ -242,3 +242,44 @@ def test_binding_refuses_what_ctypes_would_cut():
                  lambda: x.kv4_attention(q, c, 0, stream=other)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+class Recorder:
+    """Stands in for the library: keeps what the attention was called with."""
+
+    def __init__(self, need=16):
+        self.calls, self.need = [], need
+
+    def fdl_kv4_attention(self, h, desc, q, cache, kv_len, out, lse, ws, ws_bytes, stream):
+        d = desc._obj
+        self.calls.append((d.block_start, d.window_left, d.window_right, d.sinks, d.scale))
+        return 0
+
+    def fdl_kv4_attention_workspace_bytes(self, h, desc):
+        return self.need
+
+
+def host_context(monkeypatch, lib):
+    """A context whose calls go to `lib` with CPU tensors, and a cache for it."""
+    import types
+    monkeypatch.setattr(fdllm, "_lib", lib)
+    monkeypatch.setattr(fdllm, "_raw_stream", lambda device: 0)
+    x = fdllm.Context.__new__(fdllm.Context)
+    x.device, x._h, x._kv4_descs, x._seeds = -1, None, {}, {}
+    c = types.SimpleNamespace(batch=1, n_kv_heads=2, seq_len=100, head_dim=64, device_index=-1,
+                              buffers=fdllm.Kv4Buffers())
+    return x, c, torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16)
+
+
+def test_arguments_are_read_at_every_call(monkeypatch):
+    """Tensors as numbers, changed in place between two calls."""
+    lib = Recorder()
+    x, c, q = host_context(monkeypatch, lib)
+    start, left, right, sinks = (torch.tensor(v) for v in (8, 5, 6, 4))
+    scale = torch.tensor(0.5)
+    x.kv4_attention(q, c, start, window=(left, right), sinks=sinks, scale=scale)
+    for t in (start, left, right, sinks):
+        t += 10
+    scale += 0.5
+    x.kv4_attention(q, c, start, window=(left, right), sinks=sinks, scale=scale)
+    assert lib.calls == [(8, 5, 6, 4, 0.5), (18, 15, 16, 14, 1.0)]
