@@ -278,8 +278,11 @@ def test_arguments_are_read_at_every_call(monkeypatch):
     start, left, right, sinks = (torch.tensor(v) for v in (8, 5, 6, 4))
     scale = torch.tensor(0.5)
     x.kv4_attention(q, c, start, window=(left, right), sinks=sinks, scale=scale)
-    for t in (start, left, right, sinks):
+    for t in (left, right, sinks):
         t += 10
     scale += 0.5
     x.kv4_attention(q, c, start, window=(left, right), sinks=sinks, scale=scale)
-    assert lib.calls == [(8, 5, 6, 4, 0.5), (18, 15, 16, 14, 1.0)]
+    assert lib.calls == [(8, 5, 6, 4, 0.5), (8, 15, 16, 14, 1.0)]
+    start += 10
+    x.kv4_attention(q, c, start, window=(left, right), sinks=sinks, scale=scale)
+    assert lib.calls[2:] == [(18, 15, 16, 14, 1.0)]
