@@ -683,6 +683,33 @@ fdl::Kv4Ptrs kv4_ptrs(const fdl_kv4_cache* c) {
                         (uint8_t*)c->v_scale};
 }
 
+// The dimensions of rows that have more than one entry, by ascending stride.
+struct RowDim { long long stride; int count; };
+int row_dims(const fdl::Kv4Rows& r, RowDim* dims) {
+    const RowDim all[3] = {{r.seq_stride, r.batch}, {r.row_stride, r.n}, {r.head_stride, r.heads}};
+    int k = 0;
+    for (const RowDim& d : all) {
+        if (d.count < 2) continue;
+        int at = k++;
+        for (; at > 0 && dims[at - 1].stride > d.stride; --at) dims[at] = dims[at - 1];
+        dims[at] = d;
+    }
+    return k;
+}
+
+// Whether rows may share elements: unless each stride is at least what the smaller
+// ones, and a row's head_dim, span.
+bool rows_overlap(const fdl::Kv4Rows& r) {
+    RowDim dims[3];
+    const int k = row_dims(r, dims);
+    __int128 span = r.head_dim;
+    for (int i = 0; i < k; ++i) {
+        if (dims[i].stride < span) return true;
+        span += (__int128)dims[i].stride * (dims[i].count - 1);
+    }
+    return false;
+}
+
 // Checks the rows [start, start + n) of a store or load and resolves their strides.
 int kv4_rows(const char* who, const fdl_ctx* ctx, const fdl_kv4_rows_desc* d, int start, int n,
              bool written, fdl::Kv4Rows* out) {
@@ -715,9 +742,9 @@ int kv4_rows(const char* who, const fdl_ctx* ctx, const fdl_kv4_rows_desc* d, in
     if (r.seq_stride < 0 || r.row_stride < 0 || r.head_stride < 0 || r.seq_stride % per16 ||
         r.row_stride % per16 || r.head_stride % per16)
         return fail(FDL_EINVAL, "%s: strides must be >= 0 and multiples of 16 bytes", who);
-    if (written && ((r.batch > 1 && !r.seq_stride) || (n > 1 && r.row_stride < r.head_dim) ||
-                    (r.heads > 1 && r.head_stride < r.head_dim)))
-        return fail(FDL_EINVAL, "%s: the rows written must not overlap", who);
+    if (written && rows_overlap(r))
+        return fail(FDL_EINVAL, "%s: the rows written must not overlap: each stride at least what "
+                    "the smaller ones span", who);
     *out = r;
     return FDL_OK;
 }

@@ -286,3 +286,35 @@ def test_arguments_are_read_at_every_call(monkeypatch):
     start += 10
     x.kv4_attention(q, c, start, window=(left, right), sinks=sinks, scale=scale)
     assert lib.calls[2:] == [(18, 15, 16, 14, 1.0)]
+
+
+@pytest.mark.parametrize("b,h,n,strides,ok", [
+    (2, 4, 10, (5120, 512, 128), True),                      # [b, n, Hkv, d]
+    (2, 4, 10, (5120, 128, 1280), True),                     # [b, Hkv, n, d]
+    (2, 4, 10, (128, 256, 2560), True),                      # [Hkv, n, b, d]
+    (2, 4, 10, (10000, 136, 1600), True),                    # with room between
+    (2, 4, 10, (1 << 61, 1 << 55, 1 << 50), True),
+    (1, 1, 10, (0, 128, 0), True),                           # a single one has no stride
+    (2, 4, 10, (5120, 128, 128), False),                     # row on row of the next head
+    (2, 4, 10, (8, 512, 128), False),                        # sequences 8 elements apart
+    (2, 4, 10, (5120 - 8, 512, 128), False),
+    (2, 4, 10, (5120, 504, 128), False),
+    (2, 4, 10, (5120, 512, 120), False),
+    (2, 4, 10, (5120, 128, 1272), False),
+    (2, 1, 10, (0, 128, 0), False),
+])
+def test_load_refuses_rows_that_overlap(monkeypatch, b, h, n, strides, ok):
+    """What passes the check goes on to the device, of which there is none here; the places of
+    the rows, where they can be listed, agree."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    L = fdllm.load()
+    d = rows(batch=b, n_kv_heads=h, seq_stride=strides[0], row_stride=strides[1],
+             head_stride=strides[2])
+    rc = L.fdl_kv4_load(ctx(), d, cache(), 0, n, P, 1 << 45, None)
+    assert rc == (fdllm.FDL_ECUDA if ok else EINVAL)
+    assert ok == (b"overlap" not in L.fdl_last_error())
+    if max(strides) < 1 << 20:
+        at = np.add.outer(np.add.outer(np.arange(b) * strides[0], np.arange(n) * strides[1]),
+                          np.arange(h) * strides[2]).ravel()[:, None] + np.arange(128)
+        assert ok == (len(np.unique(at)) == at.size)
