@@ -710,6 +710,27 @@ bool rows_overlap(const fdl::Kv4Rows& r) {
     return false;
 }
 
+// Whether a row of one copy of the rows meets a row of another, `delta` elements on:
+// the sum of strides that comes within head_dim of delta. With strides as above (no
+// overlap within a copy) what the smaller ones add is less than one step of a larger,
+// so only the two steps around the rest can reach it.
+bool copies_meet(const RowDim* dims, int k, __int128 delta, int head_dim) {
+    if (k == 0) return delta < head_dim && -delta < head_dim;
+    const RowDim& d = dims[k - 1];
+    __int128 x = delta / d.stride;
+    if (x * d.stride > delta) --x;
+    for (int i = 0; i < 2; ++i, ++x)
+        if (x < d.count && -x < d.count && copies_meet(dims, k - 1, delta - x * d.stride, head_dim))
+            return true;
+    return false;
+}
+bool copies_overlap(const fdl::Kv4Rows& r, const void* a, const void* b) {
+    RowDim dims[3];
+    const int k = row_dims(r, dims);
+    return copies_meet(dims, k, ((__int128)(uintptr_t)b - (__int128)(uintptr_t)a) / (r.bf16 ? 2 : 4),
+                       r.head_dim);
+}
+
 // Checks the rows [start, start + n) of a store or load and resolves their strides.
 int kv4_rows(const char* who, const fdl_ctx* ctx, const fdl_kv4_rows_desc* d, int start, int n,
              bool written, fdl::Kv4Rows* out) {
@@ -813,6 +834,8 @@ int fdl_kv4_load(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const fdl_kv4_cach
     if (!k_out && !v_out) return fail(FDL_EINVAL, "kv4_load: k_out and v_out are both NULL");
     if (!aligned16(k_out) || !aligned16(v_out))
         return fail(FDL_EINVAL, "kv4_load: k_out and v_out must be 16-byte aligned");
+    if (k_out && v_out && copies_overlap(r, k_out, v_out))
+        return fail(FDL_EINVAL, "kv4_load: k_out and v_out must not overlap");
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(FDL_ECUDA, "kv4_load: cannot select device");
     const cudaError_t e = fdl::launch_kv4_load(r, kv4_ptrs(cache), k_out, v_out,

@@ -432,8 +432,9 @@ FDL_API int fdl_kv4_store(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const voi
  * desc->dtype (exact in both types).
  *   k_out, v_out [b, n, Hkv, d] dtype, device, 16-byte aligned, strides as in desc
  *                (rows must not overlap: of the dimensions with more than one entry
- *                each stride is at least what the smaller ones and head_dim span);
- *                either may be NULL (not read)
+ *                each stride is at least what the smaller ones and head_dim span; nor
+ *                do k_out's and v_out's, which may be interleaved); either may be
+ *                NULL (not read)
  * Errors: as fdl_kv4_store. */
 FDL_API int fdl_kv4_load(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const fdl_kv4_cache* cache,
                          int start, int n, void* k_out, void* v_out, void* stream);

@@ -318,3 +318,36 @@ def test_load_refuses_rows_that_overlap(monkeypatch, b, h, n, strides, ok):
         at = np.add.outer(np.add.outer(np.arange(b) * strides[0], np.arange(n) * strides[1]),
                           np.arange(h) * strides[2]).ravel()[:, None] + np.arange(128)
         assert ok == (len(np.unique(at)) == at.size)
+
+
+def _places(b, h, n, strides, d=64):
+    return (np.add.outer(np.add.outer(np.arange(b) * strides[0], np.arange(n) * strides[1]),
+                         np.arange(h) * strides[2]).ravel()[:, None] + np.arange(d)).ravel()
+
+
+def test_load_refuses_k_and_v_on_top_of_one_another():
+    """K's and V's rows interleaved in one buffer in every way, and the ways that overlap: refused
+    exactly where a place occurs in both."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    L = fdllm.load()
+    rng = np.random.default_rng(5)
+    seen = {True: 0, False: 0}
+    for _ in range(1500):
+        b, h, n = (int(x) for x in rng.integers(1, 4, 3))
+        strides, span = [0, 0, 0], 64
+        for i in rng.permutation(3):
+            strides[i] = span + 8 * int(rng.choice([0, 0, 1, 8, 24, 9 * int(rng.integers(1, 8))]))
+            span = strides[i] * (b, n, h)[i]
+        delta = 8 * int(rng.integers(-span // 8 - 20, span // 8 + 21))
+        at = _places(b, h, n, strides)
+        ok = not np.intersect1d(at, at + delta).size
+        d = rows(batch=b, n_kv_heads=h, head_dim=64, seq_stride=strides[0], row_stride=strides[1],
+                 head_stride=strides[2])
+        k = 1 << 40
+        rc = L.fdl_kv4_load(ctx(), d, cache(), 0, n, k, k + 2 * delta, None)
+        assert rc == (fdllm.FDL_ECUDA if ok else EINVAL), (b, h, n, strides, delta)
+        seen[ok] += 1
+    assert min(seen.values()) > 300
+    assert L.fdl_kv4_load(ctx(), rows(), cache(), 0, 10, P, P, None) == EINVAL
+    assert L.fdl_kv4_load(ctx(), rows(), cache(), 0, 10, P, P + 100 * 1024, None) == fdllm.FDL_ECUDA
