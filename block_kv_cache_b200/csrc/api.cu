@@ -859,7 +859,11 @@ int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q
     if (!rc) rc = check_kv4_cache("kv4_attention", cache);
     if (rc) return rc;
     if (!q || !out) return fail(FDL_EINVAL, "kv4_attention: q and out must be non-NULL");
-    if (q == out) return fail(FDL_EINVAL, "kv4_attention: out must not be q");
+    // a block may read its rows of q when others have written theirs of out
+    const uint64_t q_bytes = (uint64_t)s.batch * s.n_q_heads * s.block_len * s.head_dim * 2;
+    const uintptr_t qa = (uintptr_t)q, oa = (uintptr_t)out;
+    if ((qa > oa ? qa - oa : oa - qa) < q_bytes)
+        return fail(FDL_EINVAL, "kv4_attention: out must not overlap q");
     if (!aligned16(q) || !aligned16(out) || ((uintptr_t)lse & 3u) || ((uintptr_t)kv_len & 3u))
         return fail(FDL_EINVAL, "kv4_attention: q and out must be 16-byte aligned, lse and "
                     "kv_len 4-byte aligned");

@@ -471,7 +471,7 @@ FDL_API size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx,
  * whose block sees nothing gets out = 0 and lse = -inf.
  *   q       [b, B, Hq, d]  bf16, device, 16-byte aligned
  *   kv_len  [b] int32, device, optional (NULL: L); clamped to [0, L]
- *   out     [b, B, Hq, d]  bf16, device, 16-byte aligned (written; not q)
+ *   out     [b, B, Hq, d]  bf16, device, 16-byte aligned (written; no part of q)
  *   lse     [b, Hq, B] f32, device, optional: log sum_j exp(scale q.k_j)
  *   ws      device scratch of >= fdl_kv4_attention_workspace_bytes(desc) bytes,
  *           16-byte aligned (NULL where that is 16); calls that may overlap on the

@@ -351,3 +351,17 @@ def test_load_refuses_k_and_v_on_top_of_one_another():
     assert min(seen.values()) > 300
     assert L.fdl_kv4_load(ctx(), rows(), cache(), 0, 10, P, P, None) == EINVAL
     assert L.fdl_kv4_load(ctx(), rows(), cache(), 0, 10, P, P + 100 * 1024, None) == fdllm.FDL_ECUDA
+
+
+def test_attention_refuses_out_that_overlaps_q():
+    L = fdllm.load()
+    d, size, q = attn(), 2 * 32 * 8 * 128 * 2, 1 << 40
+    for delta in (0, 16, -16, size - 16, 16 - size):
+        assert L.fdl_kv4_attention(ctx(), d, q, cache(), None, q + delta, None, P, 1 << 30,
+                                   None) == EINVAL
+    assert b"overlap" in L.fdl_last_error()
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    for delta in (size, -size):
+        assert L.fdl_kv4_attention(ctx(), d, q, cache(), None, q + delta, None, P, 1 << 30,
+                                   None) == fdllm.FDL_ECUDA
