@@ -149,7 +149,9 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
     const int own = min(a.chunk_rows, a.rows - row0);                 // rows that exist
     const int mine_rows = (own + a.cluster - 1 - rank) / a.cluster;   // rows rank, rank + cluster..
     const uint32_t bar = sb + S::OFF_BAR;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::OFF_BAR + 8);
     if (a.cluster > 1 && threadIdx.x == 0) {
+        *abort_flag = 0;
         sm100::mbar_init(bar, 1);
         sm100::fence_barrier_init();
         // every split of the cluster sends a row of D + 2 floats for each of them
@@ -551,9 +553,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
         }
     }
     if (a.cluster > 1) {
-        // ---- the rows that this block joins, once every split has sent them. On the
-        // way out of a wait that ran out too, nothing may land in a block that left.
-        const bool got = sm100::mbar_wait_drain(bar, 0, a.err);
+        // ---- the rows that this block joins, once every split has sent them
+        const bool got = sm100::mbar_wait(bar, 0, abort_flag, a.err);
         for (int it = threadIdx.x; got && it < mine_rows * (D / 4); it += A4_THREADS) {
             const int k = it / (D / 4), c = it % (D / 4), r = k * a.cluster + rank;
             float M = -INFINITY, sum = 0.f;
@@ -580,6 +581,14 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                     acc.w += v[x].w * f;
                 }
             finish(r, c, acc, M, sum);
+        }
+        if (!got) {
+            // Nothing may land in a block that left: the others have sent their rows once
+            // each of their threads has come here too or left, and what was sent lands.
+            // (An arrival of every block's, waited for by all of them: 0.2 us more.)
+            sm100::cluster_arrive();
+            sm100::cluster_wait();
+            sm100::mbar_wait_drain(bar, 0, a.err);
         }
     }
     if (threadIdx.x == 0) FDL_TL(0, 6);

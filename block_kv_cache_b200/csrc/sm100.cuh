@@ -143,8 +143,9 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // Wait of the give-up path: for an asynchronous operation this thread (or a
-// copy it requested) has already started and that completes by itself (a TMA
-// load landing, a tcgen05 commit arriving), so that nothing is still on its
+// copy it requested) has already started, or another block that has come to a
+// barrier since, and that completes by itself (a TMA load or a st.async
+// landing, a tcgen05 commit arriving), so that nothing is still on its
 // way into the CTA's shared memory or TMEM when the CTA leaves. Ignores the
 // abort flag and has the fixed limit kWaitTimeoutNs (records DEV_TIMEOUT and
 // returns false if even that runs out).

@@ -628,3 +628,33 @@ def test_attention_of_exact_scores_under_any_scale(ctx, b, hq, hkv, d, L, start,
     c, q = exact_scores(b, hq, hkv, d, L, B, 162, 0)
     out, lse = ctx.kv4_attention(q, c, start, want_lse=True, scale=scale)
     check_exact_scores(q, c, out, lse, float(np.float32(scale)))
+
+
+@pytest.mark.parametrize("b,hq,hkv,d,L,B", [
+    (1, 32, 32, 128, 768, 32),           # a cluster per unit
+    (2, 4, 4, 64, 500, 16),
+    (1, 7, 1, 128, 9000, 1),             # clusters of 2 and a join of their parts; rows of one rank
+])
+def test_a_wait_of_few_rows_that_runs_out_is_reported(b, hq, hkv, d, L, B):
+    """The wait for the other blocks' rows follows the context's limit: limited to 1 ns, either
+    it did not run out (a poll may last until its barrier is there) and the result is right, or
+    the host reads FDL_ETIMEOUT; calls after it, and a new context's, are right."""
+    F = fdl()
+    c, q = random_cache(b, hkv, L, d, seed=171), queries(b, B, hq, d, 172)
+    x = F.Context(0)
+    x.set_wait_timeout(1)
+    for _ in range(20):
+        out, lse = x.kv4_attention(q, c, 200, want_lse=True)
+        try:
+            x.device_status()
+        except F.FdlError as e:
+            assert e.code == F.FDL_ETIMEOUT
+            break
+        check_attention(q, c, out, lse, 200, seqs=range(1))
+    x.close()
+    torch.cuda.synchronize()
+    x = F.Context(0)
+    out, lse = x.kv4_attention(q, c, 200, want_lse=True)
+    check_attention(q, c, out, lse, 200, seqs=range(1))
+    x.device_status()
+    x.close()
