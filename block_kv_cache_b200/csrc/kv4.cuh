@@ -2,7 +2,8 @@
 //
 // Along head_dim every 16 values share one scale:
 //   scale = e4m3(max |x| / 6)    round to nearest even, at most 448
-//   code  = e2m1(x / scale)      round to nearest even, at most 6; 0 where scale = 0
+//   code  = e2m1(x / scale)      round to nearest even, at most 6; 0 where x = 0 or the
+//                                scale is 0 or NaN; -0 (8) where x < 0 rounds to 0
 // and stand for code * scale. e2m1 holds {0, .5, 1, 1.5, 2, 3, 4, 6} and their
 // negatives (2 significant bits), e4m3 4 significant bits, so a product has at
 // most 6 and lies on the grid 2^-10 up to 2688: bf16 and f16 hold every one

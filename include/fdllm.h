@@ -393,7 +393,8 @@ FDL_API int fdl_full_attention(fdl_ctx* ctx, const fdl_attn_desc* desc, const vo
  * scale:
  *   scale = e4m3(max |x| / 6)   8 bits, round to nearest even, at most 448
  *   code  = e2m1(x / scale)     4 bits, round to nearest even, at most 6;
- *                               0 where scale = 0
+ *                               0 where x = 0 or the scale is 0 or NaN; -0 (8)
+ *                               where x < 0 rounds to 0
  * and stand for code * scale, which bf16 holds exactly. e2m1 codes 0..7 are 0,
  * 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign. Values beyond 6 * 448 = 2688 and
  * infinities saturate; a NaN makes its group's scale NaN (0x7f), and the whole

@@ -2,7 +2,8 @@
 block attention over its visible positions. numpy only; every rounding is the definition's.
 
 Groups of 16 along the last dimension share scale = e4m3(max |x| / 6) (to nearest even, at most
-448); code = e2m1(x / scale) (to nearest even, at most 6; 0 where the scale is 0).
+448); code = e2m1(x / scale) (to nearest even, at most 6; 0 where x is 0 or the scale 0 or NaN, -0
+where x < 0 rounds to 0).
 """
 from __future__ import annotations
 
@@ -36,7 +37,7 @@ def kv4_quantise(x):
         s = E4M3[scale][..., None]
         r = np.where(s > 0, np.abs(g) / np.where(s > 0, s, 1.0), 0.0)
         code = _nearest_even(np.minimum(np.nan_to_num(r, posinf=1e300), 6.0), E2M1)
-    code = (code | np.where((g < 0) & (code > 0), 8, 0)).reshape(x.shape).astype(np.uint8)
+    code = (code | np.where((g < 0) & (s > 0), 8, 0)).reshape(x.shape).astype(np.uint8)
     return code[..., 0::2] | (code[..., 1::2] << 4), scale
 
 

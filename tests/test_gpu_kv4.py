@@ -658,3 +658,27 @@ def test_a_wait_of_few_rows_that_runs_out_is_reported(b, hq, hkv, d, L, B):
     check_attention(q, c, out, lse, 200, seqs=range(1))
     x.device_status()
     x.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_are_the_oracles_bytes(ctx, d, dtype):
+    """Under every scale, both signs, with what rounds to 0: a negative value keeps its sign, a
+    -0, and whatever is in a group whose scale is 0 or NaN, has none."""
+    steps = np.concatenate([[0.0, 1e-30, 0.1, 0.24, 0.25, 0.26, 0.5], np.linspace(0.3, 6, 40)])
+    groups = []
+    for s in range(1, 127):
+        x = np.concatenate([steps, -steps]) * K.E4M3[s]
+        x = np.concatenate([x, np.full(-len(x) % 15, -0.0)]).reshape(-1, 15)
+        groups.append(np.concatenate([np.full((len(x), 1), -6 * K.E4M3[s]), x], 1))
+    tiny = np.resize([-1e-3, 1e-3, -2.0 ** -100, -0.0, 0.0], (5, 16))
+    nan = np.resize([-1.0, np.nan, 2.0, -0.0, -np.inf], (5, 16))
+    g = np.concatenate(groups + [tiny, -tiny, nan, -nan])
+    g = np.concatenate([g, np.full((-len(g) % (d // 16), 16), -0.0)]).reshape(-1, d)
+    g = torch.from_numpy(g).to(dtype).double().numpy()
+    got, want = store_rows(ctx, g, dtype), O.kv4_quantise(g)
+    np.testing.assert_array_equal(got[1], want[1])
+    np.testing.assert_array_equal(got[0], want[0])
+    nib = np.stack((got[0] & 15, got[0] >> 4), -1).reshape(g.shape)
+    zero = np.repeat((got[1] == 0) | (got[1] == 127), 16, -1)
+    assert zero.any() and (nib[zero | (g == 0)] == 0).all() and (nib[~zero & (g < 0)] >= 8).all()

@@ -365,3 +365,13 @@ def test_attention_refuses_out_that_overlaps_q():
     for delta in (size, -size):
         assert L.fdl_kv4_attention(ctx(), d, q, cache(), None, q + delta, None, P, 1 << 30,
                                    None) == fdllm.FDL_ECUDA
+
+
+def test_quantise_signs_of_zeros():
+    x = np.resize([6.0, -0.1, 0.1, -0.0, 0.0, -1.0], 16)
+    codes, _ = O.kv4_quantise(x)
+    nib = np.stack((codes & 15, codes >> 4), -1).ravel()
+    np.testing.assert_array_equal(nib, np.resize([7, 8, 0, 0, 0, 10], 16))
+    for y in (x * 1e-4, np.concatenate([x[:15], [np.nan]])):               # scales 0 and NaN
+        codes, scale = O.kv4_quantise(y)
+        assert scale[0] in (0, 127) and not codes.any()
