@@ -850,6 +850,16 @@ size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx, const fdl_kv4_attn_
     return fdl::kv4_attention_workspace_bytes(s, fdl::kv4_attention_plan(s, ctx->sm_count));
 }
 
+int fdl_kv4_attention_plan(const fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, fdl_kv4_plan* plan) {
+    if (!ctx || !plan) return fail(FDL_EINVAL, "kv4_attention plan: ctx or plan is NULL");
+    fdl::Kv4Attn s;
+    const int rc = check_kv4_attn(desc, &s);
+    if (rc) return rc;
+    const fdl::Kv4Plan p = fdl::kv4_attention_plan(s, ctx->sm_count);
+    *plan = fdl_kv4_plan{p.many ? 1 : 0, p.mt, p.n_splits, p.cluster};
+    return FDL_OK;
+}
+
 int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q,
                       const fdl_kv4_cache* cache, const int32_t* kv_len, void* out, float* lse,
                       void* ws, size_t ws_bytes, void* stream) {

@@ -35,7 +35,7 @@ EXPORTS = ("fdl_abi_version", "fdl_create", "fdl_destroy", "fdl_last_error",
            "fdl_full_attention", "fdl_ffn", "fdl_qkv_attention", "fdl_model_create",
            "fdl_model_destroy", "fdl_generate_workspace_bytes", "fdl_generate",
            "fdl_kv4_store", "fdl_kv4_load", "fdl_kv4_attention_workspace_bytes",
-           "fdl_kv4_attention", "fdl_generate_workspace_bytes_kv")
+           "fdl_kv4_attention_plan", "fdl_kv4_attention", "fdl_generate_workspace_bytes_kv")
 
 
 class AttnDesc(ctypes.Structure):
@@ -46,7 +46,7 @@ class AttnDesc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
-ABI_VERSION = 7
+ABI_VERSION = 8
 KV4_MAX_SEQ = 1 << 30
 
 
@@ -70,6 +70,12 @@ class Kv4AttnDesc(ctypes.Structure):
                 ("block_len", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("scale", ctypes.c_float), ("window_left", ctypes.c_int),
                 ("window_right", ctypes.c_int), ("sinks", ctypes.c_int)]
+
+
+class Kv4Plan(ctypes.Structure):
+    """fdl_kv4_plan: which kernel takes an attention over a 4-bit cache, and its splits."""
+    _fields_ = [("many_rows", ctypes.c_int), ("row_tiles", ctypes.c_int),
+                ("splits", ctypes.c_int), ("cluster", ctypes.c_int)]
 
 
 class LMHeadDesc(ctypes.Structure):
@@ -193,6 +199,7 @@ def load() -> ctypes.CDLL:
                                vp, vp, vp]
     L.fdl_kv4_attention_workspace_bytes.argtypes = [vp, ctypes.POINTER(Kv4AttnDesc)]
     L.fdl_kv4_attention_workspace_bytes.restype = sz
+    L.fdl_kv4_attention_plan.argtypes = [vp, ctypes.POINTER(Kv4AttnDesc), ctypes.POINTER(Kv4Plan)]
     L.fdl_kv4_attention.argtypes = [vp, ctypes.POINTER(Kv4AttnDesc), vp,
                                     ctypes.POINTER(Kv4Buffers), vp, vp, vp, vp, sz, vp]
     for name in EXPORTS:
@@ -559,6 +566,11 @@ class Context:
 
     def kv4_attention_workspace_bytes(self, desc: Kv4AttnDesc) -> int:
         return int(load().fdl_kv4_attention_workspace_bytes(self._h, ctypes.byref(desc)))
+
+    def kv4_attention_plan(self, desc: Kv4AttnDesc) -> Kv4Plan:
+        plan = Kv4Plan()
+        _check(load().fdl_kv4_attention_plan(self._h, ctypes.byref(desc), ctypes.byref(plan)))
+        return plan
 
     def kv4_attention(self, q, cache: Kv4Cache, block_start, *, kv_len=None, window=(-1, -1),
                       sinks=0, out=None, lse=None, want_lse=False, scale=0.0, ws=None,

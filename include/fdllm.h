@@ -42,7 +42,7 @@
 extern "C" {
 #endif
 
-#define FDL_ABI_VERSION 7
+#define FDL_ABI_VERSION 8
 
 #if defined(__GNUC__)
 #define FDL_API __attribute__((visibility("default")))
@@ -460,6 +460,18 @@ typedef struct {
  * 0 for an invalid context or descriptor. */
 FDL_API size_t fdl_kv4_attention_workspace_bytes(const fdl_ctx* ctx,
                                                  const fdl_kv4_attn_desc* desc);
+
+/* How fdl_kv4_attention runs a shape on ctx's device, for tests and measurements. */
+typedef struct {
+    int many_rows;  /* 1: the tcgen05 kernel, 0: the one for few query rows per kv head */
+    int row_tiles;  /* tiles of 128 (many_rows) or 16 query rows of a block of threads */
+    int splits;     /* blocks that share the positions of one unit of rows */
+    int cluster;    /* ... of which so many join on chip, and the rest in ws */
+} fdl_kv4_plan;
+
+/* Errors: FDL_EINVAL (null), and those of fdl_kv4_attention for the descriptor. */
+FDL_API int fdl_kv4_attention_plan(const fdl_ctx* ctx, const fdl_kv4_attn_desc* desc,
+                                   fdl_kv4_plan* plan);
 
 /* Block attention over a 4-bit cache (fdl_dualcache_attention's counterpart): for
  * each sequence b, q-head h and block row i,

@@ -375,3 +375,24 @@ def test_quantise_signs_of_zeros():
     for y in (x * 1e-4, np.concatenate([x[:15], [np.nan]])):               # scales 0 and NaN
         codes, scale = O.kv4_quantise(y)
         assert scale[0] in (0, 127) and not codes.any()
+
+
+def test_plan_query():
+    """What the query says of both kernels' shapes on 148 SMs, and its refusals."""
+    L = fdllm.load()
+
+    def plan(**kw):
+        p = fdllm.Kv4Plan()
+        assert L.fdl_kv4_attention_plan(ctx(), attn(**kw), ctypes.byref(p)) == 0
+        return p
+    p = plan(batch=1, seq_len=1 << 20, block_len=1)
+    assert (p.many_rows, p.row_tiles, p.cluster) == (0, 1, 2) and p.splits > 8
+    assert plan().many_rows == 0 and plan().row_tiles == 2
+    p = plan(batch=32, n_q_heads=28, seq_len=1024)
+    assert (p.many_rows, p.row_tiles, p.splits, p.cluster) == (1, 2, 1, 1)
+    assert L.fdl_kv4_attention_plan(None, attn(), ctypes.byref(p)) == EINVAL
+    assert L.fdl_kv4_attention_plan(ctx(), attn(), None) == EINVAL
+    assert L.fdl_kv4_attention_plan(ctx(), None, ctypes.byref(p)) == EINVAL
+    assert L.fdl_kv4_attention_plan(ctx(), attn(head_dim=96), ctypes.byref(p)) == EUNSUP
+    body = re.search(r"typedef struct \{([^}]*)\} fdl_kv4_plan;", _header()).group(1)
+    assert re.findall(r"int (\w+);", body) == [f for f, _ in fdllm.Kv4Plan._fields_]
