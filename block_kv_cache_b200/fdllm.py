@@ -357,7 +357,7 @@ class Context:
         self._ws = None
         self._seeds = {}        # empty tensors by dtype, from which others are made: an
                                 # allocation without a dtype to read takes 1.4 us, not 2
-        self._kv4_descs = {}    # descriptors by their values, as references for the calls
+        self._kv4_descs = {}    # descriptors by their values: a reference for the calls, scratch
 
     def close(self):
         if getattr(self, "_h", None):
@@ -600,12 +600,13 @@ class Context:
         block_start = int(block_start)
         key = (b, B, Hq, hd, cache.batch, cache.n_kv_heads, cache.seq_len, cache.head_dim,
                block_start, left, right, sinks, scale)
-        d = self._kv4_descs.get(key)
-        if d is None:
+        known = self._kv4_descs.get(key)
+        if known is None:
             if len(self._kv4_descs) >= 4096:
                 self._kv4_descs.clear()
-            d = self._kv4_descs[key] = ctypes.byref(
-                self.kv4_attn_desc(q, cache, block_start, (left, right), sinks, scale))
+            d = self.kv4_attn_desc(q, cache, block_start, (left, right), sinks, scale)
+            known = self._kv4_descs[key] = ctypes.byref(d), self.kv4_attention_workspace_bytes(d)
+        d, need = known
         if kv_len is not None:
             self._here(kv_len, "kv_len", torch.int32, (b,))
         if out is None:
@@ -616,21 +617,15 @@ class Context:
             self._here(lse, "lse", torch.float32, (b, Hq, B))
         elif want_lse:
             lse = self._seed(torch.float32).new_empty(b, Hq, B)
-        L = _lib or load()
-        args = (self._h, d, q.data_ptr(), ctypes.byref(cache.buffers),
-                None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
-                None if lse is None else lse.data_ptr())
-        if ws is None:
-            # most shapes need no scratch and say so by taking none
-            rc = L.fdl_kv4_attention(*args, None, 0, _raw_stream(self.device))
-            if rc == FDL_EWORKSPACE:
-                n = int(L.fdl_kv4_attention_workspace_bytes(self._h, d))
-                ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-        else:
-            self._here(ws, "ws", ws.dtype, ws.shape)
         if ws is not None:
-            rc = L.fdl_kv4_attention(*args, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     _raw_stream(self.device))
+            self._here(ws, "ws", ws.dtype, ws.shape)
+        elif need > 16:                      # most shapes need none
+            ws = self._seed(torch.uint8).new_empty(need)
+        rc = (_lib or load()).fdl_kv4_attention(
+            self._h, d, q.data_ptr(), ctypes.byref(cache.buffers),
+            None if kv_len is None else kv_len.data_ptr(), out.data_ptr(),
+            None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(self.device))
         if rc:
             _check(rc)
         return (out, lse) if (want_lse or lse is not None) else out

@@ -396,3 +396,20 @@ def test_plan_query():
     assert L.fdl_kv4_attention_plan(ctx(), attn(head_dim=96), ctypes.byref(p)) == EUNSUP
     body = re.search(r"typedef struct \{([^}]*)\} fdl_kv4_plan;", _header()).group(1)
     assert re.findall(r"int (\w+);", body) == [f for f, _ in fdllm.Kv4Plan._fields_]
+
+
+def test_scratch_is_asked_for_once_and_without_an_error(monkeypatch):
+    """A shape's scratch is known before its first call: one call reaches the library, and none
+    that is refused (whose text would stay behind as the last error)."""
+    for need in (16, 4096):
+        lib = Recorder(need)
+        sizes, asked = [], []
+        lib.fdl_kv4_attention = lambda *a: sizes.append((a[7] is not None, a[8])) or \
+            (EWS if a[8] < need and need > 16 else 0)
+        lib.fdl_kv4_attention_workspace_bytes = lambda *a: asked.append(1) or need
+        x, c, q = host_context(monkeypatch, lib)
+        x._seeds[torch.uint8] = torch.empty(0, dtype=torch.uint8)
+        for _ in range(3):
+            x.kv4_attention(q, c, 8)
+        assert sizes == 3 * [(need > 16, need if need > 16 else 0)]
+        assert len(asked) == 1
