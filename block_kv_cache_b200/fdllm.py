@@ -266,7 +266,12 @@ class Kv4Cache:
     """One layer's K/V cache in microscaled 4-bit floating point (fdl_kv4_cache): codes k, v
     [b, Hkv, L, d/2] and scales k_scale, v_scale [b, Hkv, L, d/16], uint8 CUDA tensors that the
     caller may own (Kv4Cache(k, k_scale, v, v_scale)) or have allocated here (Kv4Cache.empty,
-    zeroed: every position reads as 0 until it is stored)."""
+    zeroed: every position reads as 0 until it is stored). It stays with these tensors and
+    their memory: another Kv4Cache is made for others."""
+    k = property(lambda self: self._tensors[0])
+    k_scale = property(lambda self: self._tensors[1])
+    v = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     def __init__(self, k, k_scale, v, v_scale):
         try:
@@ -284,7 +289,7 @@ class Kv4Cache:
             right = False
         if not right:
             self._refuse(k, k_scale, v, v_scale)
-        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        self._tensors = k, k_scale, v, v_scale
         self.batch, self.n_kv_heads, self.seq_len, self.head_dim = b, h, L, 2 * half
         self.device_index = dev
         self.buffers = Kv4Buffers(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(),

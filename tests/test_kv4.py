@@ -413,3 +413,13 @@ def test_scratch_is_asked_for_once_and_without_an_error(monkeypatch):
             x.kv4_attention(q, c, 8)
         assert sizes == 3 * [(need > 16, need if need > 16 else 0)]
         assert len(asked) == 1
+
+
+def test_a_caches_tensors_are_not_replaced():
+    """The calls go to the addresses that the cache was made with."""
+    c = fdllm.Kv4Cache.__new__(fdllm.Kv4Cache)
+    c._tensors = tuple(torch.full((1,), i) for i in range(4))
+    for i, name in enumerate(("k", "k_scale", "v", "v_scale")):
+        assert getattr(c, name) is c._tensors[i]
+        with pytest.raises(AttributeError):
+            setattr(c, name, torch.zeros(1))
