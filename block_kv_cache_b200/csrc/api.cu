@@ -683,6 +683,19 @@ fdl::Kv4Ptrs kv4_ptrs(const fdl_kv4_cache* c) {
                         (uint8_t*)c->v_scale};
 }
 
+// Whether two of a cache's buffers share bytes: read they may, written they are at once.
+bool cache_overlaps(const fdl::Kv4Rows& r, const fdl_kv4_cache* c) {
+    const uint64_t rows = (uint64_t)r.batch * r.heads * r.seq_len;
+    const uintptr_t at[4] = {(uintptr_t)c->k, (uintptr_t)c->v, (uintptr_t)c->k_scale,
+                             (uintptr_t)c->v_scale};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < i; ++j) {
+            const int lo = at[i] < at[j] ? i : j, hi = i + j - lo;
+            if (at[hi] - at[lo] < rows * (lo < 2 ? r.head_dim / 2 : r.head_dim / 16)) return true;
+        }
+    return false;
+}
+
 // The dimensions of rows that have more than one entry, by ascending stride.
 struct RowDim { long long stride; int count; };
 int row_dims(const fdl::Kv4Rows& r, RowDim* dims) {
@@ -818,6 +831,8 @@ int fdl_kv4_store(fdl_ctx* ctx, const fdl_kv4_rows_desc* desc, const void* k_new
     if (!k_new || !v_new) return fail(FDL_EINVAL, "kv4_store: NULL buffer");
     if (!aligned16(k_new) || !aligned16(v_new))
         return fail(FDL_EINVAL, "kv4_store: k_new and v_new must be 16-byte aligned");
+    if (cache_overlaps(r, cache))
+        return fail(FDL_EINVAL, "kv4_store: the cache's buffers must not overlap");
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(FDL_ECUDA, "kv4_store: cannot select device");
     const cudaError_t e = fdl::launch_kv4_store(r, k_new, v_new, kv4_ptrs(cache),

@@ -407,7 +407,8 @@ typedef struct {
     void* k_scale;  /* [b, Hkv, L, d/16] uint8: e4m3 scales */
     void* v;        /* as k */
     void* v_scale;  /* as k_scale */
-} fdl_kv4_cache;    /* device, every buffer 16-byte aligned, owned by the caller */
+} fdl_kv4_cache;    /* device, every buffer 16-byte aligned, owned by the caller; none
+                       overlaps another where rows are stored */
 
 typedef struct {
     int batch;           /* b >= 1, at most 65535 */

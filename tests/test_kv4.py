@@ -423,3 +423,23 @@ def test_a_caches_tensors_are_not_replaced():
         assert getattr(c, name) is c._tensors[i]
         with pytest.raises(AttributeError):
             setattr(c, name, torch.zeros(1))
+
+
+def test_store_refuses_a_cache_on_top_of_itself():
+    """K's and V's rows are written at once: their codes and scales lie apart."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    L = fdllm.load()
+    codes, scales, at = 2 * 4 * 100 * 64, 2 * 4 * 100 * 8, 1 << 40
+
+    def store(k, ks, v, vs):
+        return L.fdl_kv4_store(ctx(), rows(), P, P, 0, 10,
+                               cache(k=at + k, k_scale=at + ks, v=at + v, v_scale=at + vs), None)
+    apart = (0, codes, codes + scales, 2 * codes + scales)
+    assert store(*apart) == store(apart[2], apart[3], apart[0], apart[1]) == fdllm.FDL_ECUDA
+    for bad in ((0, 2 * codes, 0, 3 * codes), (0, 2 * codes, codes, 2 * codes),
+                (0, 2 * codes, codes - 16, 3 * codes), (codes - 16, 2 * codes, 0, 3 * codes),
+                (0, codes, 2 * codes, codes + scales - 16), (0, codes - 16, 2 * codes, 3 * codes),
+                (16, 0, 2 * codes, 3 * codes)):
+        assert store(*bad) == EINVAL
+        assert b"overlap" in L.fdl_last_error()
