@@ -111,14 +111,31 @@ int parts_of(const Kv4Plan& p) { return p.n_splits / p.cluster; }
 Kv4Plan kv4_attention_plan(const Kv4Attn& s, int sm_count) {
     Kv4Plan p;
     const int rows = s.block_len * (s.n_q_heads / s.n_kv_heads), seen = most_seen(s);
-    // The tcgen05 kernel takes 7 to 10 us before it is any faster: it is used where the
-    // 32-row blocks of the other would not all run at once (tcgen05 and the other, 64
-    // units of 128 rows over 1024 positions: 16.0 and 29.3 us) or have much to do (32
-    // units of 64 rows over 4096: 22.5 and 25.8; 32 of 128 over 1024: 13.5 and 15.4;
-    // below the edge, 8 units of 256 rows over 1024: 17.0 and 11.9; just above it, 8 of
-    // 128 over 4096: 17.6 and 16.4).
+    // The tcgen05 kernel has the longer first and last parts. It is used where the 32-row
+    // blocks of the other would not all run at once, or have much to do: positions times
+    // blocks per SM beyond an edge that depends on the tiles of rows and the head size.
+    // us, tcgen05 and the other:
+    //   one block per unit (up to 32 rows), never: 32 heads of 128 over 2048 positions
+    //     14.1 and 10.8, over 131072 300 and 245; heads of 64 276 and 166
+    //   more blocks than SMs: 40 units of 128 rows x 128 over 1024 13.7 and 26.9, 24 of
+    //     224 over 256 12.5 and 13.9; the worst there is, 160 units of 40 rows x 64, one
+    //     more round of blocks on 148 SMs, over 1024 28.0 and 25.3
+    //   128 rows x 128, edge 850: 32 units over 900 (778) 12.9 and 13.4, over 1200 (1038)
+    //     13.7 and 15.8; 8 units over 2048 (443) 15.5 and 10.6, over 5200 (1124) 17.9 and
+    //     17.4, over 6000 18.5 and 18.8
+    //   256 rows x 128, edge 1700: 8 units of 224 over 4096 (1550) 23.8 and 22.8, over 5000
+    //     (1892) 25.0 and 26.4; 16 units over 2048 (1550) 28.1 and 21.6, over 3000 (2270)
+    //     30.4 and 29.2, over 4096 32.5 and 36.9
+    //   128 rows x 64, edge 1500: 32 units over 1200 (1038) 11.3 and 10.3, over 1800 (1557)
+    //     12.7 and 13.6; 8 units over 6000 (1297) 15.3 and 12.7, over 10000 (2162) 17.1
+    //     and 17.8
+    //   256 rows x 64, edge 2600: 8 units of 224 over 6000 (2270) 21.5 and 20.4, over 8000
+    //     (3027) 22.3 and 25.5; 16 units over 3000 (2270) 24.5 and 19.5, over 5000 (3784)
+    //     28.3 and 29.5
     const long long blocks = (long long)s.batch * s.n_kv_heads * ((rows + 31) / 32);
-    p.many = rows > 32 && (blocks > sm_count || blocks * seen > 850ll * sm_count);
+    const long long edge = s.head_dim == 128 ? (rows <= 128 ? 850 : 1700)
+                                             : (rows <= 128 ? 1500 : 2600);
+    p.many = rows > 32 && (blocks > sm_count || blocks * seen > edge * sm_count);
     if (p.many) {
         p.chunks = (rows + 255) / 256;
         p.chunk_rows = (rows + p.chunks - 1) / p.chunks;

@@ -23,8 +23,8 @@ VARIANTS = [
         (1, 1, "alone", (19, 20, 4, 190, 101, 17)),      # 85
         (1, 2, "cluster", (6, 28, 4, 700, 411, 32)),     # 224, 24 units
         (1, 1, "cluster", (10, 16, 4, 700, 411, 31)),    # 124, 40 units
-        (1, 2, "parts", (2, 64, 8, 2300, 1300, 31)),     # 248, 16 units
-        (1, 1, "parts", (4, 16, 4, 4300, 2500, 31)),     # 124, 16 units
+        (1, 2, "parts", (2, 64, 8, 6300, 3300, 31)),     # 248, 16 units
+        (1, 1, "parts", (4, 16, 4, 7300, 4100, 31)),     # 124, 16 units
         (0, 2, "alone", (19, 8, 8, 190, 101, 29)),       # 29
         (0, 1, "alone", (19, 16, 8, 190, 101, 7)),       # 14
         (0, 2, "cluster", (5, 12, 4, 700, 411, 9)),      # 27

@@ -443,3 +443,19 @@ def test_store_refuses_a_cache_on_top_of_itself():
                 (16, 0, 2 * codes, 3 * codes)):
         assert store(*bad) == EINVAL
         assert b"overlap" in L.fdl_last_error()
+
+
+@pytest.mark.parametrize("d,hq,b,hkv,below,above", [
+    (128, 32, 1, 8, 3900, 4000), (128, 28, 1, 4, 8900, 9100),            # edges 850 and 1700
+    (64, 32, 4, 8, 1700, 1800), (64, 28, 4, 4, 3400, 3500),              # 1500 and 2600
+])
+def test_the_plan_changes_kernels_where_it_was_measured(d, hq, b, hkv, below, above):
+    L = fdllm.load()
+
+    def many(n, **kw):
+        p = fdllm.Kv4Plan()
+        assert L.fdl_kv4_attention_plan(ctx(), attn(batch=b, n_q_heads=hq, n_kv_heads=hkv,
+                                                    head_dim=d, seq_len=n, **kw), ctypes.byref(p)) == 0
+        return p.many_rows
+    assert (many(below), many(above)) == (0, 1)
+    assert many(1 << 20, window_left=20, window_right=0) == 0            # what is seen counts
