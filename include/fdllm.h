@@ -399,6 +399,12 @@ FDL_API int fdl_full_attention(fdl_ctx* ctx, const fdl_attn_desc* desc, const vo
  * 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign. Values beyond 6 * 448 = 2688 and
  * infinities saturate; a NaN makes its group's scale NaN (0x7f), and the whole
  * group reads as NaN; groups whose largest value is at most 3 * 2^-9 read as 0.
+ * What is read back is off by at most 17/96 of its group's largest |x| (one step
+ * between the codes 4 and 6, under a scale rounded to 4 bits), 9 % of the rows'
+ * size for normally distributed ones; where that largest is below 6 * 2^-6 the
+ * scale is subnormal, a multiple of 2^-9, and the error at most the larger of
+ * max |x| / 6 + 2^-10 and 6 * 2^-10. There is no second scale per tensor: rows that
+ * lie below that, or above 2688, have to be scaled by the caller.
  * ------------------------------------------------------------------------ */
 #define FDL_KV4_MAX_SEQ (1 << 30)   /* positions: the kernels count them in 32 bits */
 

@@ -682,3 +682,32 @@ def test_codes_are_the_oracles_bytes(ctx, d, dtype):
     nib = np.stack((got[0] & 15, got[0] >> 4), -1).reshape(g.shape)
     zero = np.repeat((got[1] == 0) | (got[1] == 127), 16, -1)
     assert zero.any() and (nib[zero | (g == 0)] == 0).all() and (nib[~zero & (g < 0)] >= 8).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,L,B", [(4, 4, 128, 600, 32), (8, 2, 64, 500, 7),
+                                          (7, 1, 128, 900, 1)])
+def test_attention_against_unquantised_rows(ctx, hq, hkv, d, L, B):
+    """What the 4 bits cost: with every cached element off by at most 17/96 of its group's largest
+    (e_k, e_v), a score moves by at most dz = scale sum |q| e_k, a probability by a factor of at most
+    e^(2 dz), so |out - ref| <= sum p e_v + (e^(2 dz) - 1) sum p (|v| + e_v), and the log-sum-exp by dz;
+    beside them the kernel's own rounding (here below 2^-6 of sum p |v| and 2^-10)."""
+    rng = np.random.default_rng(181)
+    k, v = (torch.from_numpy(rng.standard_normal((1, L, hkv, d))).to(torch.bfloat16) for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((1, B, hq, d)) / 8).to(torch.bfloat16)
+    c = fdl().Kv4Cache.empty(1, hkv, L, d)
+    ctx.kv4_store(k.cuda(), v.cuda(), c, 0)
+    out, lse = ctx.kv4_attention(q.cuda(), c, 0, want_lse=True)
+    qn, kn, vn = (t[0].double().numpy() for t in (q, k, v))
+    kn, vn = kn.transpose(1, 0, 2), vn.transpose(1, 0, 2)
+
+    def off(x):
+        return np.repeat(np.abs(x).reshape(hkv, L, d // 16, 16).max(-1) * 17 / 96, 16, -1)
+    ref, rl, spread = O.kv4_attention(qn, kn, vn, np.ones(L, bool))
+    e_v, _, _ = O.kv4_attention(qn, kn, off(vn), np.ones(L, bool))
+    # sum p e_v with the probabilities of kn: the values' bounds in the values' place
+    dz = np.zeros((B, hq))
+    for h in range(hq):
+        dz[:, h] = (np.abs(qn[:, h]) @ off(kn)[h // (hq // hkv)].T).max(1) * d ** -0.5
+    tol = e_v + np.expm1(2 * dz)[..., None] * (spread + e_v) + 2.0 ** -6 * spread + 2.0 ** -10
+    assert (np.abs(out[0].double().cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(lse[0].double().cpu().numpy() - rl) <= dz.T + 2.0 ** -10).all()

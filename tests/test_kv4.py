@@ -459,3 +459,22 @@ def test_the_plan_changes_kernels_where_it_was_measured(d, hq, b, hkv, below, ab
         return p.many_rows
     assert (many(below), many(above)) == (0, 1)
     assert many(1 << 20, window_left=20, window_right=0) == 0            # what is seen counts
+
+
+def test_quantisation_error_is_the_documented_one():
+    """With scale = (max / 6)(1 + e), |e| <= 2^-4, a quotient is at most 6 / (1 - 2^-4) = 6.4 and
+    its code off by at most 1 (between 4 and 6; 0.4 beyond 6): scale <= 17/96 max. A subnormal
+    scale is off by up to 2^-10, which a code of 6 multiplies."""
+    rng = np.random.default_rng(3)
+    for exponent in range(-14, 12):
+        x = rng.standard_normal((2000, 16)) * 2.0 ** exponent * rng.uniform(0.5, 1, (2000, 1))
+        x = np.concatenate([x, rng.uniform(-1, 1, (2000, 16)) * 2.0 ** exponent])
+        x = np.clip(x, -2688, 2688)
+        err = np.abs(O.kv4_values(*O.kv4_quantise(x)) - x).max(1)
+        top = np.abs(x).max(1)
+        bound = np.where(top >= 6 * 2.0 ** -6, top * 17 / 96,
+                         np.maximum(top / 6 + 2.0 ** -10, 6 * 2.0 ** -10))
+        assert (err <= bound * (1 + 1e-12)).all(), exponent
+        if -3 < exponent < 8:
+            rel = np.linalg.norm(O.kv4_values(*O.kv4_quantise(x[:2000])) - x[:2000])
+            assert 0.08 < rel / np.linalg.norm(x[:2000]) < 0.10
