@@ -205,3 +205,26 @@ def test_captured_and_replayed(ctx, case):
             torch.cuda.synchronize()
             check_attention(q, c, out, lse, v.start, n, seqs=range(min(v.b, 2)))
     ctx.device_status()
+
+
+def test_two_calls_at_once(ctx, case):
+    """Two streams' calls, each with its own scratch, and a store between, do not disturb one
+    another."""
+    v, c = case
+    cs, qs = [copy_of(c) for _ in range(2)], [queries(v.b, v.B, v.hq, v.d, 41 + i) for i in range(2)]
+    rows = [queries(v.b, v.B, v.hkv, v.d, 43 + i) for i in range(2)]
+    streams, got, want = [torch.cuda.Stream() for _ in range(2)], [[], []], []
+    for i in range(2):
+        ctx.kv4_store(rows[i], rows[i], cs[i], v.start)
+        want.append(attend(ctx, v, qs[i], cs[i]))
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for i in range(2):
+            ctx.kv4_store(rows[i], rows[i], cs[i], v.start, stream=streams[i])
+            got[i].append(ctx.kv4_attention(qs[i], cs[i], v.start, want_lse=True,
+                                            stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+    ctx.device_status()
