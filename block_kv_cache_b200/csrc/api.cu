@@ -740,8 +740,8 @@ bool copies_meet(const RowDim* dims, int k, __int128 delta, int head_dim) {
 bool copies_overlap(const fdl::Kv4Rows& r, const void* a, const void* b) {
     RowDim dims[3];
     const int k = row_dims(r, dims);
-    return copies_meet(dims, k, ((__int128)(uintptr_t)b - (__int128)(uintptr_t)a) / (r.bf16 ? 2 : 4),
-                       r.head_dim);
+    const __int128 bytes = (__int128)(uintptr_t)b - (__int128)(uintptr_t)a;
+    return copies_meet(dims, k, bytes / (r.bf16 ? 2 : 4), r.head_dim);
 }
 
 // Checks the rows [start, start + n) of a store or load and resolves their strides.

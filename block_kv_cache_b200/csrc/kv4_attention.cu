@@ -37,13 +37,16 @@
 // workspace and a second kernel joins them.
 //
 // What bounds it (heads of 128; 6.55 TB/s measured copy): one token of 28 heads over
-// 131072 positions of 4, 75.5 MB: 25.2 us with the join. 18 of them in the steps (4.2
-// TB/s), where the schedulers issue in 62 % of the cycles, the pipe that converts is
-// busy for half and the tensor pipe for 42 %: dependent work of four warps each, and
-// 128 registers allow no fifth. 2.3 before the first step, 2.4 for the join. A block of
-// 32 rows over 768 positions: 7.7 us, of them 1.5 for Q, 2.4 for the merge. Two blocks
-// of 8 warps per SM with up to 16 rows (one of 8: 29 us; one of 16: 25.2, and 26.2
-// with its warps held to within two steps of one another, so that no block is done
+// 131072 positions of 4, 75.5 MB: 25.7 us with the join. 18 of them in the steps (4.2
+// TB/s), where neither the issue slots (49 % over the whole kernel) nor the tensor pipe
+// (32 %) are full: dependent work of four warps a scheduler, and 128 registers (20 bytes
+// spilled) allow no fifth. Half of the 64 that hold outputs are rows 8 to 15, which the
+// 7 heads of a group do not fill; the queries as the 8 columns would free them. 2.3
+// before the first step, 2.4 for the join. A block of 32 rows over 768 positions: 7.8
+// us, of them 1.5 for Q, 2.4 for the merge; over 131072 positions of 32 heads 246 (92 for
+// the bytes; steps of 16 positions, one block of 8 warps per SM). Two blocks of 8 warps
+// per SM with up to 16 rows (one of 8: 29 us; one of 16: 25.2 where this was 25.2, and
+// 26.2 with its warps held to within two steps of one another, so that no block is done
 // early); with 32 rows the outputs take the registers of one.
 //
 // Numbers: cached values are exact in f16 (kv4.cuh). Queries are brought to f16
@@ -221,7 +224,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                     cp_async<S::SB>(st + S::OFF_VS + lane * S::SB, vs + at, true);
                 } else {                     // K's scales by half of the lanes, V's by the other
                     const size_t at = (p0 + (lane & 15)) * S::SB;
-                    cp_async<S::SB>(st + S::OFF_KS + lane * S::SB, (lane < 16 ? ks : vs) + at, true);
+                    cp_async<S::SB>(st + S::OFF_KS + lane * S::SB, (lane < 16 ? ks : vs) + at,
+                                    true);
                 }
             } else {
 #pragma unroll
@@ -320,7 +324,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                 const uint8_t* ka = st + S::OFF_K + row * S::CB;
                 if constexpr (D == 128) {
                     lds(ka + ((t ^ (row & 2)) << 4), kw[nt]);
-                    sc[nt] = *reinterpret_cast<const uint16_t*>(st + S::OFF_KS + row * S::SB + 2 * t);
+                    sc[nt] = *reinterpret_cast<const uint16_t*>(st + S::OFF_KS + row * S::SB +
+                                                                2 * t);
                 } else {
                     lds(ka + 8 * t, kw[nt]);
                     sc[nt] = st[S::OFF_KS + row * S::SB + t] * 0x0101u;
@@ -334,7 +339,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
-                        lds(smem + S::OFF_Q + ((mt * S::KK + 2 * w + x) * 32 + lane) * 16, qf[mt][x]);
+                        lds(smem + S::OFF_Q + ((mt * S::KK + 2 * w + x) * 32 + lane) * 16,
+                            qf[mt][x]);
 #pragma unroll
                 for (int nt = 0; nt < S::NT; ++nt) {
                     uint32_t b[4];
@@ -597,7 +603,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
 template <int D, int MT>
 int capacity(int c) {
     static std::atomic<int> known[9];
-    return kv4_clusters((const void*)kv4_attn_kernel<D, MT>, A4_THREADS, A4<D, MT>::TOTAL, c, known);
+    return kv4_clusters((const void*)kv4_attn_kernel<D, MT>, A4_THREADS, A4<D, MT>::TOTAL, c,
+                        known);
 }
 
 template <int D, int MT>

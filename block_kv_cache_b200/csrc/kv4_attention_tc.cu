@@ -23,20 +23,22 @@
 //
 // What bounds it, in us:
 //   32 sequences, 32 queries of 28 heads on 4 kv heads of 128, 1024 positions: 24.4
-//     (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the bytes). 3.7
+//     (9.3 for the products at the measured 1615 TFLOP/s, 2.9 for the bytes). 3.5
 //     before the first scores (Q's rows, their powers of two; 1.5 before that for the
-//     launch), 16 tiles at 1.05 each, 2.3 for the output. A tile: two softmax warps on a scheduler take 1450
-//     cycles when nothing else issues (measured alone), the conversion's share of
-//     it is 500 more.
-//   8 sequences, 32 queries of 32 heads on 8, a window of 1060 positions: 15.5, two
+//     launch), 16 tiles at 1.0 each, 2.3 for the output. A tile: two softmax warps on a
+//     scheduler take 1450 cycles when nothing else issues (measured alone), the
+//     conversion's share of it is 500 more.
+//   8 sequences, 32 queries of 32 heads on 8, a window of 1060 positions: 15.6, two
 //     blocks of 128 rows each: 3.0 before the first scores, 5.9 for 9 tiles, 5.0 for
 //     the output and the join.
+// The 128 registers do not hold all of three forms (heads and tiles: 64, 1 spills 32
+// bytes, 64, 2 4, 128, 1 28).
 // The first and last parts run once through fresh instructions, so they are kept
 // short: a row of Q comes as one bulk copy (16 bytes per lane with cp.async: first
-// scores 1.1 later), a row's output leaves TMEM as bf16 and the block as one bulk copy per row (4.9
-// -> 2.5 with the stores 8 bytes per lane), and the weights of a join are found by
-// the lanes of one warp (3.0 -> 2.4; rows pushed to the block that joins them with
-// st.async: 2.6 for the pushes alone). Measured and not kept: four conversion warps
+// scores 1.1 later), a row's output leaves TMEM as bf16 and the block as one bulk copy
+// per row (4.9 -> 2.5 with the stores 8 bytes per lane), and the weights of a join are
+// found by the lanes of one warp (3.0 -> 2.4; rows pushed to the block that joins them
+// with st.async: 2.6 for the pushes alone). Measured and not kept: four conversion warps
 // (28.2 and 18.2), K and V converted by different warps (26.2 and 17.3) or their
 // pieces in turn (25.7 and 16.6); the search for the next tile's maximum beside this
 // one's exponentials (1.5 more).
@@ -187,7 +189,7 @@ kv4_attn_tc_kernel(const Kv4AttnArgs a) {
         FDL_TL(0, 0);
         for (int t = 0; t < ST; ++t) {
             mbar_init(kv_full(t), 4);
-                        mbar_init(kv_free(t), MT);
+            mbar_init(kv_free(t), MT);
         }
         for (int w = 0; w < 2; ++w)
             for (int j = 0; j < 2; ++j) {

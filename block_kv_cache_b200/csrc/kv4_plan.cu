@@ -123,9 +123,9 @@ Kv4Plan kv4_attention_plan(const Kv4Attn& s, int sm_count) {
     //   128 rows x 128, edge 850: 32 units over 900 (778) 12.9 and 13.4, over 1200 (1038)
     //     13.7 and 15.8; 8 units over 2048 (443) 15.5 and 10.6, over 5200 (1124) 17.9 and
     //     17.4, over 6000 18.5 and 18.8
-    //   256 rows x 128, edge 1700: 8 units of 224 over 4096 (1550) 23.8 and 22.8, over 5000
-    //     (1892) 25.0 and 26.4; 16 units over 2048 (1550) 28.1 and 21.6, over 3000 (2270)
-    //     30.4 and 29.2, over 4096 32.5 and 36.9
+    //   256 rows x 128, edge 1850: 8 units of 224 over 4096 (1550) 23.8 and 22.8, over 5000
+    //     (1892) 25.0 and 26.4; 16 of 256 over 2048 (1771) 30.5 and 21.8, 16 of 224 over
+    //     3000 (2270) 30.4 and 29.2, over 4096 32.5 and 36.9
     //   128 rows x 64, edge 1500: 32 units over 1200 (1038) 11.3 and 10.3, over 1800 (1557)
     //     12.7 and 13.6; 8 units over 6000 (1297) 15.3 and 12.7, over 10000 (2162) 17.1
     //     and 17.8
@@ -133,7 +133,7 @@ Kv4Plan kv4_attention_plan(const Kv4Attn& s, int sm_count) {
     //     (3027) 22.3 and 25.5; 16 units over 3000 (2270) 24.5 and 19.5, over 5000 (3784)
     //     28.3 and 29.5
     const long long blocks = (long long)s.batch * s.n_kv_heads * ((rows + 31) / 32);
-    const long long edge = s.head_dim == 128 ? (rows <= 128 ? 850 : 1700)
+    const long long edge = s.head_dim == 128 ? (rows <= 128 ? 850 : 1850)
                                              : (rows <= 128 ? 1500 : 2600);
     p.many = rows > 32 && (blocks > sm_count || blocks * seen > edge * sm_count);
     if (p.many) {
@@ -157,7 +157,7 @@ Kv4Plan kv4_attention_plan(const Kv4Attn& s, int sm_count) {
                       : kv4_few_clusters(s.head_dim, p.mt, c);
     };
     // Many splits: clusters of 2, which leave no SM out, and partial results of each
-    // (a token over 131072 positions of 4 kv heads: 27.3 us; of 4: 28.2, of 8: 28.3).
+    // (a token over 131072 positions of 4 kv heads: 25.8 us; of 4: 27.9, of 8: 28.4).
     if (n > 8) {
         const long long fit = clusters(2) / p.units, want = n / 2;
         p.cluster = 2;

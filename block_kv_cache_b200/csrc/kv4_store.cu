@@ -249,7 +249,8 @@ cudaError_t launch_rows(const Kv4Rows& s, const void* k_src, const void* v_src, 
                   s.heads, s.seq_len, s.start, s.n, head_blocks};
     void (*kfn)(const Kv4RowsArgs);
     if constexpr (STORE)
-        kfn = s.bf16 ? (s.head_dim == 128 ? kv4_store_kernel<bf16, 128> : kv4_store_kernel<bf16, 64>)
+        kfn = s.bf16 ? (s.head_dim == 128 ? kv4_store_kernel<bf16, 128>
+                                          : kv4_store_kernel<bf16, 64>)
                      : (s.head_dim == 128 ? kv4_store_kernel<float, 128>
                                           : kv4_store_kernel<float, 64>);
     else

@@ -303,8 +303,8 @@ class Kv4Cache:
                 raise TypeError(f"Kv4Cache: {n} must be a contiguous uint8 CUDA tensor on k's "
                                 "device")
         raise ValueError("Kv4Cache: k and v must be [b, Hkv, L, d/2], the scales [b, Hkv, L, "
-                         f"d/16], d 64 or 128, no dimension above 2^30; not {tuple(k.shape)}, {tuple(k_scale.shape)}, "
-                         f"{tuple(v.shape)}, {tuple(v_scale.shape)}")
+                         f"d/16], d 64 or 128, no dimension above 2^30; not {tuple(k.shape)}, "
+                         f"{tuple(k_scale.shape)}, {tuple(v.shape)}, {tuple(v_scale.shape)}")
 
     @classmethod
     def empty(cls, batch, n_kv_heads, seq_len, head_dim=128, device="cuda"):

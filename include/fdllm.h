@@ -409,7 +409,8 @@ FDL_API int fdl_full_attention(fdl_ctx* ctx, const fdl_attn_desc* desc, const vo
 #define FDL_KV4_MAX_SEQ (1 << 30)   /* positions: the kernels count them in 32 bits */
 
 typedef struct {
-    void* k;        /* [b, Hkv, L, d/2] uint8: codes, the even dimension of a pair in the low nibble */
+    void* k;        /* [b, Hkv, L, d/2] uint8: codes, the even dimension of a pair in the
+                       low nibble */
     void* k_scale;  /* [b, Hkv, L, d/16] uint8: e4m3 scales */
     void* v;        /* as k */
     void* v_scale;  /* as k_scale */

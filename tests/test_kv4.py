@@ -446,7 +446,7 @@ def test_store_refuses_a_cache_on_top_of_itself():
 
 
 @pytest.mark.parametrize("d,hq,b,hkv,below,above", [
-    (128, 32, 1, 8, 3900, 4000), (128, 28, 1, 4, 8900, 9100),            # edges 850 and 1700
+    (128, 32, 1, 8, 3900, 4000), (128, 28, 1, 4, 9700, 9800),            # edges 850 and 1850
     (64, 32, 4, 8, 1700, 1800), (64, 28, 4, 4, 3400, 3500),              # 1500 and 2600
 ])
 def test_the_plan_changes_kernels_where_it_was_measured(d, hq, b, hkv, below, above):
