@@ -37,6 +37,7 @@ struct fdl_ctx {
     size_t acc_bytes;
     unsigned* d_sync;        // grid-barrier words of the fused kernels (zeroed)
     GenGraph* gen;           // cached device-loop decode graph, or NULL
+    uint64_t wait_ns;        // the wait limit, as at d_err + 8
 };
 
 // Split-K accumulator of the few-token projections (zeroed at creation; every
@@ -157,6 +158,7 @@ int fdl_create(fdl_ctx** out, int device) {
     c->d_sync = nullptr;
     c->gen = nullptr;
     c->acc_bytes = kAccBytes;
+    c->wait_ns = kDefaultWaitNs;
     // 16 bytes: the error word, then (8-byte aligned) the limit of the
     // kernels' progress waits in ns
     const uint64_t limit = kDefaultWaitNs;
@@ -206,6 +208,7 @@ int fdl_set_wait_timeout(fdl_ctx* ctx, uint64_t ns) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e == cudaSuccess)
         e = cudaMemcpy(reinterpret_cast<char*>(ctx->d_err) + 8, &ns, 8, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) ctx->wait_ns = ns;
     return e == cudaSuccess ? FDL_OK : cuda_fail(e, "set_wait_timeout");
 }
 
@@ -898,6 +901,7 @@ int fdl_kv4_attention(fdl_ctx* ctx, const fdl_kv4_attn_desc* desc, const void* q
         return fail(FDL_EWORKSPACE, "kv4_attention: workspace needs %zu bytes (16-byte aligned), "
                     "got %zu", need, ws ? ws_bytes : (size_t)0);
     s.kv_len = kv_len;
+    s.polled = ctx->wait_ns < 1000000;
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(FDL_ECUDA, "kv4_attention: cannot select device");
     const cudaError_t e = fdl::launch_kv4_attention(s, plan, q, kv4_ptrs(cache), out, lse,

@@ -560,7 +560,8 @@ kv4_attn_kernel(const Kv4AttnArgs a) {
     }
     if (a.cluster > 1) {
         // ---- the rows that this block joins, once every split has sent them
-        const bool got = sm100::mbar_wait(bar, 0, abort_flag, a.err);
+        const bool got = a.polled ? sm100::mbar_poll(bar, 0, abort_flag, a.err)
+                                  : sm100::mbar_wait(bar, 0, abort_flag, a.err);
         for (int it = threadIdx.x; got && it < mine_rows * (D / 4); it += A4_THREADS) {
             const int k = it / (D / 4), c = it % (D / 4), r = k * a.cluster + rank;
             float M = -INFINITY, sum = 0.f;

@@ -28,6 +28,7 @@ struct Kv4AttnArgs {
     int parts;                   // n_splits / cluster: partial results left in the workspace
     int sinks, win_lo, win_hi;
     float scale_log2;
+    int polled;                  // the context's wait limit is a shortened one
     int* err;
 };
 

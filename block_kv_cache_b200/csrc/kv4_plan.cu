@@ -239,6 +239,7 @@ cudaError_t launch_kv4_attention(const Kv4Attn& s, const Kv4Plan& p, const void*
     a.win_lo = s.win_lo;
     a.win_hi = s.win_hi;
     a.scale_log2 = fminf(s.scale * 1.4426950408889634f, 3.4028234663852886e38f);
+    a.polled = s.polled;
     a.err = err;
     a.part = (float*)ws;
     a.part_ml = (float4*)((float*)ws + (size_t)p.units * a.parts * a.chunk_rows * s.head_dim);

@@ -88,6 +88,7 @@ struct Kv4Attn {
     int batch, n_q_heads, n_kv_heads, head_dim, seq_len, block_len;
     int sinks, win_lo, win_hi;   // 0 <= win_lo <= win_hi <= L, 0 <= sinks <= L
     float scale;                 // resolved (never 0)
+    int polled;                  // the context's wait limit is below 1 ms
     const int32_t* kv_len;
 };
 // Query the cluster capacities that the plans use (outside any stream capture).

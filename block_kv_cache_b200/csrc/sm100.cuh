@@ -142,6 +142,22 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     }
 }
 
+// mbar_wait by polls that return at once, for a shortened limit: a try_wait may be
+// suspended until its barrier is there, whatever the limit.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int* err) {
+    const uint64_t t0 = globaltimer(), limit = wait_limit_ns(err);
+    while (!mbar_test(bar, parity)) {
+        if (*abort) return false;
+        if (globaltimer() - t0 > limit) {
+            *abort = 1;
+            record_error(err, DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
 // Wait of the give-up path: for an asynchronous operation this thread (or a
 // copy it requested) has already started, or another block that has come to a
 // barrier since, and that completes by itself (a TMA load or a st.async
